@@ -524,6 +524,185 @@ moe_status moe_layer_set_timing(moe_layer* l, void* const* events, int n);
  * *status_out and clears it. */
 moe_status moe_read_device_status(moe_layer* l, void* stream, int32_t* status_out);
 
+/* ============================================================ decode block
+ * The operators that a decode block runs around the routed layer: the norms
+ * and residual additions before and after it, the attention's key-value cache
+ * in pages, and the attention's projections with 4-bit weights.  They follow
+ * the conventions above (stream-ordered, the caller owns every buffer, argument
+ * errors returned before anything is enqueued).  Strides are in elements.
+ */
+
+/* Element types (0 and 1 as in moe_nvfp4_quantize). */
+enum { MOE_DT_BF16 = 0, MOE_DT_F32 = 1, MOE_DT_F16 = 2, MOE_DT_E4M3 = 3 };
+
+/* ------------------------------------------------------------- block norm
+ * One pass over T rows of H values, between one block and the next:
+ *   b = post_norm ? N(y; w_post, b_post) : y            (the block's output)
+ *   r = res_scale * x + branch_scale * act(gate) * b    (the new residual)
+ *   h = N(r; w_pre, b_pre)                              (the next block's input)
+ *   N(v; w, c) = (v - mean) / sqrt(mean((v - mean)^2) + eps) * (w + w_offset) + c
+ * with mean = 0 for MOE_NORM_RMS.  Everything is fp32; h is taken from r
+ * before r is rounded to its type.
+ *   - y NULL: r = res_scale * x (the first norm of a stack); gate and
+ *     post_norm must then be absent.
+ *   - r NULL: not written.  h NULL: not written (the last block).  One of the
+ *     two must be given.  r may be x itself and h may be y itself (same
+ *     stride); no other overlap.
+ *   - w_* NULL: weights of 1 (w_offset is not applied); b_* NULL: 0.
+ *   - gate: element (t, i) at gate[t * gate_row + i * gate_col], gate_col 0 or
+ *     1; a stride of 0 broadcasts (one gate a channel, or one a token).
+ *     gate_act MOE_GATE_SIGMOID takes its logistic function.
+ * Types: (stream_type of x, r; branch_type of y, h, gate) is (bf16, bf16),
+ * (f16, f16), (f32, f32), (f32, bf16) or (f32, f16); weight_type (w_*, b_*)
+ * is f32 or branch_type; else MOE_ERR_UNSUPPORTED.  1 <= H <= 32768 (more:
+ * MOE_ERR_UNSUPPORTED).  T == 0 is a no-op.
+ */
+enum { MOE_NORM_RMS = 0, MOE_NORM_LAYER = 1 };
+enum { MOE_GATE_NONE = 0, MOE_GATE_SIGMOID = 1 };
+
+typedef struct {
+  int T, H;
+  int kind;                       /* MOE_NORM_*                              */
+  int stream_type, branch_type, weight_type;
+  const void* x; int64_t ldx;     /* device [T][H], row stride ldx           */
+  const void* y; int64_t ldy;     /* device [T][H] or NULL                   */
+  const void* gate;               /* device or NULL                          */
+  int64_t gate_row, gate_col;
+  int gate_act;
+  int post_norm;
+  const void* w_post; const void* b_post; /* device [H] or NULL              */
+  const void* w_pre; const void* b_pre;   /* device [H] or NULL              */
+  float res_scale, branch_scale, eps, w_offset;
+  void* r; int64_t ldr;           /* device out [T][H] or NULL               */
+  void* h; int64_t ldh;           /* device out [T][H] or NULL               */
+} moe_block_norm_args;
+
+moe_status moe_block_norm(const moe_block_norm_args* a, void* stream);
+
+/* ------------------------------------------------- paged key-value cache
+ * Keys and values of all sequences live in two pools of n_pages pages, each
+ * of page_size tokens for every kv head: token i of page p and head h starts
+ * at k_pages + p * page_stride + h * head_stride + i * token_stride (values
+ * likewise; the D values of a token are contiguous).  page_table[s * table_ld + j] is
+ * the page that holds tokens [j * page_size, (j + 1) * page_size) of sequence
+ * s.  Offsets are 64 bits wide.  kv_type is the type of q, or MOE_DT_E4M3
+ * with k_scale / v_scale [Hkv] fp32 on the device (value = code * scale; NULL
+ * for 1).
+ * D a multiple of 16, 16 <= D <= 256; strides multiples of 16 bytes and pools
+ * 16-byte aligned; else MOE_ERR_UNSUPPORTED.
+ */
+typedef struct {
+  void* k_pages; void* v_pages;
+  int64_t page_stride, head_stride, token_stride;
+  int n_pages, page_size, Hkv, D;
+  int kv_type;
+  const float* k_scale; const float* v_scale;
+} kvcache_view;
+
+/* kvcache_append stores the keys and values of N new tokens, rotated when cos
+ * and sin are given, and writes the queries rotated likewise (rotary position
+ * embedding).  Token n belongs to sequence seq[n] (NULL: sequence n) at
+ * position pos[n].  The first `rot` values of each q and k head turn in pairs
+ * (a, b) -> (a c - b s, a s + b c), c = cos[pos][i], s = sin[pos][i] (fp32,
+ * [max_pos][rot / 2]): pair i is (v[i], v[i + rot/2]), or (v[2i], v[2i + 1])
+ * with interleaved set.  fp32, rounded once (to nearest even; E4M3 after
+ * division by the scale, saturating at +-448).
+ *   - q NULL: no queries.  q_out may be q itself (same strides).
+ *   - pos[n] < 0: token n is skipped (nothing is stored, its q_out row is 0).
+ *     A sequence, position or page out of range (of n_seqs, of max_pages *
+ *     page_size and max_pos, of n_pages) is skipped likewise and sets
+ *     MOE_ERR_DEVICE in *status.
+ *   - two tokens with the same sequence and position race.
+ * rot a multiple of 16, rot <= D; q, k, v, q_out 16-byte aligned with strides
+ * of a multiple of 8 elements; else MOE_ERR_UNSUPPORTED. */
+typedef struct {
+  kvcache_view c;
+  int N, Hq;
+  int dtype;                       /* of q, k, v, q_out: MOE_DT_BF16 / MOE_DT_F16 */
+  const void* k; int64_t k_row, k_head;  /* device [N][Hkv][D]                    */
+  const void* v; int64_t v_row, v_head;
+  const void* q; int64_t q_row, q_head;  /* device [N][Hq][D] or NULL             */
+  void* q_out; int64_t q_out_row, q_out_head;
+  const int32_t* seq;              /* device [N] or NULL                          */
+  const int32_t* pos;              /* device [N]                                  */
+  const int32_t* page_table; int64_t table_ld;
+  int n_seqs, max_pages;           /* rows and columns of page_table              */
+  const float* cos; const float* sin; /* device [max_pos][rot/2] or both NULL     */
+  int rot, max_pos, interleaved;
+  int32_t* status;                 /* device sticky status word, or NULL          */
+} kvcache_append_args;
+
+moe_status kvcache_append(const kvcache_append_args* a, void* stream);
+
+/* kvcache_attend: attention of one new token of each of B sequences over the
+ * cache.  Query head g reads kv head g / (Hq / Hkv).  For positions n in
+ * [max(0, len - window), len) (window 0: all), len = seq_lens[b]:
+ *   s_n = scale * q.k_n;  softcap > 0: s_n = softcap * tanh(s_n / softcap)
+ *   out = sum_n softmax(s)_n v_n,  lse = ln sum_n exp(s_n)   (fp32)
+ * A row with no position to read (len 0, or none but bad pages) gives out 0
+ * and lse -inf, as does a row whose every score is -inf.  Cache contents outside the
+ * positions read never touch the result, NaN included.
+ *   - A page id outside [0, n_pages) leaves out that page's tokens, and a
+ *     length outside [0, max_pages * page_size] is clamped to it; both set
+ *     MOE_ERR_DEVICE in *status.
+ *   - Accumulation is fp32 and runs in a fixed order: the same call gives the
+ *     same bits.
+ *   - workspace: kvcache_attend_workspace_bytes(Hq, Hkv, D) bytes, 16-byte
+ *     aligned, whose first 4096 bytes must be zero before the first call on it
+ *     (every call leaves them zero).  Calls that share it must not overlap on
+ *     the GPU.
+ * Hq a multiple of Hkv; q and out 16-byte aligned with strides of a multiple of 8
+ * elements; else MOE_ERR_UNSUPPORTED.  The pools' strides bound the call, not
+ * the lengths. */
+typedef struct {
+  kvcache_view c;
+  int B, Hq;
+  int dtype;                       /* of q and out: MOE_DT_BF16 / MOE_DT_F16      */
+  const void* q; int64_t q_row, q_head;      /* device [B][Hq][D]                 */
+  void* out; int64_t out_row, out_head;      /* device [B][Hq][D]                 */
+  float* lse;                      /* device [B][Hq] or NULL                      */
+  const int32_t* page_table; int64_t table_ld;
+  int max_pages;
+  const int32_t* seq_lens;         /* device [B]                                  */
+  float scale, softcap;
+  int window;
+  void* workspace; size_t workspace_bytes;
+  int32_t* status;
+} kvcache_attend_args;
+
+size_t kvcache_attend_workspace_bytes(int Hq, int Hkv, int D);
+moe_status kvcache_attend(const kvcache_attend_args* a, void* stream);
+
+/* ------------------------------------------------------- 4-bit linear
+ * y[t][n] = sum_k W[n][k] x[t][k] + bias[n] for T tokens, where
+ *   W[n][k] = (value(code) - zero[n][k / group]) * scale[n][k / group].
+ * MOE_W4_U4: value = code (0..15), zero from `zeros` or 8 when NULL.
+ * MOE_W4_E2M1: value = the E2M1 number (as in the expert records), zero = 0
+ * (zeros must be NULL).
+ * Codes and zeros hold two entries a byte, entry 2j in the low nibble of byte
+ * j, rows contiguous and starting on a byte: codes [N][K/2], zeros
+ * [N][ceil(K/group / 2)].  scales [N][K/group], bias and x, y of `dtype`.
+ * Products are exact and sums fp32.  Meant for few tokens: the weights are
+ * read once for every 16 of them.
+ * K a multiple of group, group a multiple of 32, K / group <= 1024; codes and
+ * x 16-byte aligned, ldx a multiple of 8; else MOE_ERR_UNSUPPORTED.  T == 0 is
+ * a no-op. */
+enum { MOE_W4_U4 = 0, MOE_W4_E2M1 = 1 };
+
+typedef struct {
+  int T, N, K, group;
+  int dtype;                       /* MOE_DT_BF16 or MOE_DT_F16                   */
+  int format;                      /* MOE_W4_*                                    */
+  const void* x; int64_t ldx;      /* device [T][K]                               */
+  const uint8_t* codes;
+  const void* scales;
+  const uint8_t* zeros;            /* device or NULL                              */
+  const void* bias;                /* device [N] or NULL                          */
+  void* y; int64_t ldy;            /* device out [T][N]                           */
+} moe_w4_linear_args;
+
+moe_status moe_w4_linear(const moe_w4_linear_args* a, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,149 @@
+// elem.cuh - element types of the decode-block operators (MOE_DT_*), their
+// conversions and the warp-level instructions those kernels share.
+#pragma once
+
+#include "common.cuh"
+
+namespace moe {
+
+__device__ __forceinline__ float f16_to_f32(uint16_t v) {
+  float f;
+  asm("cvt.f32.f16 %0, %1;" : "=f"(f) : "h"(v));
+  return f;
+}
+// two floats -> packed 16-bit pair (a in the low half), to nearest even
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+// two floats -> two E4M3 bytes (a in the low byte), saturating at +-448
+__device__ __forceinline__ uint16_t pack_e4m3(float a, float b) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
+
+template <int DT>
+struct Elem {
+  using T = uint16_t;
+};
+template <>
+struct Elem<MOE_DT_F32> {
+  using T = float;
+};
+
+template <int DT>
+__device__ __forceinline__ float to_f32(typename Elem<DT>::T v) {
+  if constexpr (DT == MOE_DT_F32) return v;
+  else if constexpr (DT == MOE_DT_BF16) return __uint_as_float((uint32_t)v << 16);
+  else return f16_to_f32(v);
+}
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if constexpr (DT == MOE_DT_BF16) return pack_bf16(a, b);
+  else return pack_f16(a, b);
+}
+template <int DT>
+__device__ __forceinline__ float lo2(uint32_t v) {
+  return to_f32<DT>((uint16_t)v);
+}
+template <int DT>
+__device__ __forceinline__ float hi2(uint32_t v) {
+  if constexpr (DT == MOE_DT_BF16) return bf16_hi(v);
+  else return to_f32<DT>((uint16_t)(v >> 16));
+}
+template <int DT>
+__device__ __forceinline__ typename Elem<DT>::T from_f32(float f) {
+  if constexpr (DT == MOE_DT_F32) return f;
+  else return (uint16_t)pack2<DT>(f, 0.f);
+}
+
+// 8 values at p (16-byte aligned) as fp32
+template <int DT>
+__device__ __forceinline__ void load8(const void* p, float (&v)[8]) {
+  if constexpr (DT == MOE_DT_F32) {
+    const float4 a = ((const float4*)p)[0], b = ((const float4*)p)[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  } else {
+    const uint4 a = *(const uint4*)p;
+    v[0] = lo2<DT>(a.x), v[1] = hi2<DT>(a.x), v[2] = lo2<DT>(a.y), v[3] = hi2<DT>(a.y);
+    v[4] = lo2<DT>(a.z), v[5] = hi2<DT>(a.z), v[6] = lo2<DT>(a.w), v[7] = hi2<DT>(a.w);
+  }
+}
+template <int DT>
+__device__ __forceinline__ void store8(void* p, const float (&v)[8]) {
+  if constexpr (DT == MOE_DT_F32) {
+    ((float4*)p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    ((float4*)p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    *(uint4*)p = make_uint4(pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]),
+                            pack2<DT>(v[6], v[7]));
+  }
+}
+
+// ---- asynchronous 16-byte copies to shared memory -----------------------------
+// bytes = 16 copies, bytes = 0 writes zeros (src is then not read)
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// ---- warp matrix instructions ---------------------------------------------------
+// Their rate is far above what a kernel bound by reading its cache or its
+// weights once can feed: the tiles are 8 or 16 rows, tcgen05's are 64 or more.
+__device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// D[16][8] += A[16][16] * B[16][8], 16-bit operands of one type, fp32 sums
+template <int DT>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  if constexpr (DT == MOE_DT_BF16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// host: a launch's outcome, or the opt-in to dynamic shared memory of a kernel
+inline moe_status launch_status(cudaError_t e) {
+  if (e == cudaSuccess) return MOE_OK;
+  cudaGetLastError();
+  return MOE_ERR_CUDA;
+}
+
+}  // namespace moe

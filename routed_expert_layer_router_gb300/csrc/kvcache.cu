@@ -1,0 +1,816 @@
+// kvcache.cu - the paged key-value cache: kvcache_append (rotation of the new
+// tokens' q and k, k and v stored into their pages) and kvcache_attend
+// (attention of one new token of each sequence over its pages).
+// Formulas and layouts in moe.h.
+#include <atomic>
+
+#include "elem.cuh"
+#include "sm100_ptx.cuh"
+
+namespace moe {
+namespace {
+
+// ------------------------------------------------------------------ append
+// One CTA a token (and, for few tokens, a slice of its heads).  A thread owns
+// 16 values of a head - the 8 pairs that share 8 cosines and sines - and
+// walks the heads, so cos and sin are loaded once a thread.  Bound by memory:
+// q, k, v read once, q_out and the pages written once.
+constexpr int kAppendThreads = 256;
+
+template <int DT, int KV>
+__global__ void __launch_bounds__(kAppendThreads) k_append(kvcache_append_args a) {
+  using E = uint16_t;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int n = blockIdx.x;
+  const int items = a.c.D / 16;                       // threads of one head
+  const int lanes = kAppendThreads / items;           // heads walked at a time
+  const int it = threadIdx.x % items, hl = threadIdx.x / items;
+  if (hl >= lanes) return;
+  const int Hkv = a.c.Hkv, heads = a.Hq + 2 * Hkv;
+
+  const int pos = a.pos[n];
+  const int seq = a.seq ? a.seq[n] : n;
+  // token's place: page id and slot, or -1
+  int page = -1, at = 0;
+  if (pos >= 0) {
+    const int col = pos / a.c.page_size;
+    at = pos - col * a.c.page_size;
+    if (seq >= 0 && seq < a.n_seqs && col < a.max_pages && (!a.cos || pos < a.max_pos)) {
+      page = a.page_table[(int64_t)seq * a.table_ld + col];
+      if (page < 0 || page >= a.c.n_pages) page = -1;
+    }
+    if (page < 0 && threadIdx.x == 0) set_status(a.status, MOE_ERR_DEVICE);
+  }
+  const bool live = page >= 0;
+
+  // d0, d1: where this thread's two runs of 8 values start; with rotation of
+  // halves a run and its partner rot/2 further on, else 16 values in a row
+  const int half = a.rot / 2;
+  const bool turn = a.cos && it * 16 < a.rot;
+  const bool apart = turn && !a.interleaved;
+  const int d0 = apart ? it * 8 : it * 16;
+  const int d1 = apart ? d0 + half : d0 + 8;
+  float cs[8], sn[8];
+  if (turn && live) {
+    load8<MOE_DT_F32>(a.cos + (int64_t)pos * half + it * 8, cs);
+    load8<MOE_DT_F32>(a.sin + (int64_t)pos * half + it * 8, sn);
+  }
+  const int64_t base = (int64_t)page * a.c.page_stride + (int64_t)at * a.c.token_stride;
+
+  const int first = blockIdx.y * lanes + hl;
+  for (int h = first; h < heads; h += gridDim.y * lanes) {
+    const bool is_q = h < a.Hq, is_k = !is_q && h < a.Hq + Hkv;
+    const int kh = is_q ? 0 : (is_k ? h - a.Hq : h - a.Hq - Hkv);
+    if (is_q && !a.q) continue;
+    if (!is_q && !live) continue;
+    const E* src = is_q   ? (const E*)a.q + n * a.q_row + h * a.q_head
+                   : is_k ? (const E*)a.k + n * a.k_row + kh * a.k_head
+                          : (const E*)a.v + n * a.v_row + kh * a.v_head;
+    float u[8], w[8];
+    load8<DT>(src + d0, u);
+    load8<DT>(src + d1, w);
+    if (turn && live && (is_q || is_k)) {
+      if (apart) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float x = u[j], y = w[j];
+          u[j] = x * cs[j] - y * sn[j];
+          w[j] = x * sn[j] + y * cs[j];
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float x = u[2 * j], y = u[2 * j + 1];
+          u[2 * j] = x * cs[j] - y * sn[j];
+          u[2 * j + 1] = x * sn[j] + y * cs[j];
+          x = w[2 * j], y = w[2 * j + 1];
+          w[2 * j] = x * cs[j + 4] - y * sn[j + 4];
+          w[2 * j + 1] = x * sn[j + 4] + y * cs[j + 4];
+        }
+      }
+    }
+    if (is_q) {
+      if (!live)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[j] = w[j] = 0.f;
+      E* dst = (E*)a.q_out + n * a.q_out_row + h * a.q_out_head;
+      store8<DT>(dst + d0, u);
+      store8<DT>(dst + d1, w);
+    } else if constexpr (KV == MOE_DT_E4M3) {
+      const float* sc = is_k ? a.c.k_scale : a.c.v_scale;
+      const float s = sc ? sc[kh] : 1.f;
+      uint8_t* dst = (uint8_t*)(is_k ? a.c.k_pages : a.c.v_pages) + base + kh * a.c.head_stride;
+      auto put = [&](uint8_t* p, const float (&x)[8]) {
+        uint32_t lo = pack_e4m3(x[0] / s, x[1] / s) | (uint32_t)pack_e4m3(x[2] / s, x[3] / s) << 16;
+        uint32_t hi = pack_e4m3(x[4] / s, x[5] / s) | (uint32_t)pack_e4m3(x[6] / s, x[7] / s) << 16;
+        *(uint2*)p = make_uint2(lo, hi);
+      };
+      put(dst + d0, u);
+      put(dst + d1, w);
+    } else {
+      E* dst = (E*)(is_k ? a.c.k_pages : a.c.v_pages) + base + kh * a.c.head_stride;
+      store8<DT>(dst + d0, u);
+      store8<DT>(dst + d1, w);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ attend
+// Bound by reading the cache once.  The sequences' tokens are cut into tiles
+// of 64; the tiles of all (sequence, kv head) items in a row are dealt to the
+// CTAs in equal contiguous runs, so a ragged batch and one long sequence fill
+// the GPU alike.  In a CTA each of 4 warps streams 16 tokens of a tile through
+// its own ring of cp.async stages (no barrier between warps inside an item)
+// and keeps a running maximum, sum and output in registers.  The query heads
+// of a kv head are the rows of the matrix instructions, so K and V are read
+// once for all of them.  A run that covers an item writes its result; items
+// cut between CTAs leave their parts in the workspace, and the CTA that
+// finishes last adds them in run order (the same bits every time).
+constexpr int kWarps = 4, kTok = 16, kTile = kWarps * kTok;
+constexpr int kMaxCtas = 2 * kSMs;
+constexpr size_t kCtlBytes = 4096;  // one counter a CTA
+static_assert(kMaxCtas * sizeof(unsigned) <= kCtlBytes, "counters");
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <int KV, int DP>
+struct Ring {
+  static constexpr int ES = KV == MOE_DT_E4M3 ? 1 : 2;
+  static constexpr int RB = DP * ES;             // bytes of a token's row
+  static constexpr int WARP = 2 * kTok * RB;     // one stage of one warp: K and V
+  static constexpr int STAGE = kWarps * WARP;
+  // about 96 KB a CTA, so that two share an SM and ~128 KB an SM are in
+  // flight; 256-value rows of 16 bits take 3 stages and the SM alone
+  static constexpr int S = 98304 / STAGE < 3 ? 3 : (98304 / STAGE > 6 ? 6 : 98304 / STAGE);
+  static constexpr int BYTES = S * STAGE;
+};
+
+struct AttendArgs {
+  kvcache_view c;
+  int B, Hq, G, nhb;  // G query heads a kv head, in nhb blocks of rows
+  const void* q;
+  void* out;
+  float* lse;
+  int64_t q_row, q_head, out_row, out_head, table_ld;
+  const int32_t* page_table;
+  const int32_t* seq_lens;
+  int max_pages, window, q_bf16;
+  float scale, softcap;
+  unsigned* counters;
+  float* parts;
+  int32_t* status;
+};
+
+// tiles of sequence b: its window is [start, start + n)
+struct Span {
+  int start, n;
+  __device__ __forceinline__ int tiles() const { return (n + kTile - 1) / kTile; }
+};
+__device__ __forceinline__ Span span_of(const AttendArgs& a, int b) {
+  const int len0 = a.seq_lens[b];
+  const int64_t cap64 = (int64_t)a.max_pages * a.c.page_size;
+  const int cap = cap64 > 0x7fffff00 ? 0x7fffff00 : (int)cap64;  // tiles stay within int
+  const int len = min(max(len0, 0), cap);
+  if (len != len0) set_status(a.status, MOE_ERR_DEVICE);
+  Span s;
+  s.start = a.window > 0 && len > a.window ? len - a.window : 0;
+  s.n = len - s.start;
+  return s;
+}
+
+// walks tiles in (sequence, head block, tile) order
+struct Cursor {
+  int b, h, tile, nt;
+  Span s;
+  __device__ __forceinline__ void next(const AttendArgs& a, int nh) {
+    if (++tile < nt) return;
+    tile = 0;
+    if (++h < nh) return;
+    h = 0;
+    do {
+      if (++b >= a.B) return;
+      s = span_of(a, b);
+      nt = s.tiles();
+    } while (nt == 0);
+  }
+};
+
+template <int RB>
+__device__ __forceinline__ uint32_t swz(int row, int ch) {
+  // 16-byte chunk `ch` of a row, placed so that 8 rows' same chunk lie in 8
+  // different bank groups
+  if constexpr (RB == 64) return row * RB + ((ch ^ (row >> 1)) & 3) * 16;
+  else return row * RB + (ch ^ (row & 7)) * 16;
+}
+
+template <int KV, int DP, int RH>
+__global__ void __launch_bounds__(kWarps * 32) k_attend(AttendArgs a) {
+  using R = Ring<KV, DP>;
+  constexpr int MT = KV == MOE_DT_BF16 ? MOE_DT_BF16 : MOE_DT_F16;  // operands' type
+  constexpr int RB = R::RB, CPR = RB / 16, S = R::S, KS = DP / 16, NT = DP / 8;
+  constexpr int ROWS = 8 * RH, PART = ROWS * (DP + 2);
+  extern __shared__ __align__(128) uint8_t ring[];
+  float* mb = (float*)(ring + R::BYTES);  // merge buffer: RH 1: two slices of 8 rows, 2: one of 16
+  __shared__ float2 ml[kWarps][ROWS];
+  __shared__ uint32_t valid[kWarps][S];
+  __shared__ int is_last;
+
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c4 = lane & 3;
+  const int nh = a.c.Hkv * a.nhb;
+  pdl_wait();
+  pdl_launch_dependents();
+
+  // rows without tokens
+  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+    if (span_of(a, b).n > 0) continue;
+    const int per = a.c.D / 8;
+    for (int i = threadIdx.x; i < a.Hq * per; i += blockDim.x)
+      *(uint4*)((uint16_t*)a.out + b * a.out_row + (i / per) * a.out_head + (i % per) * 8) =
+          make_uint4(0, 0, 0, 0);
+    if (a.lse)
+      for (int i = threadIdx.x; i < a.Hq; i += blockDim.x)
+        a.lse[(int64_t)b * a.Hq + i] = __int_as_float(0xff800000);
+  }
+
+  // this CTA's run [u0, u1) of the U tiles
+  long long U = 0;
+  for (int b = lane; b < a.B; b += 32) U += span_of(a, b).tiles();
+#pragma unroll
+  for (int o = 16; o; o >>= 1) U += __shfl_xor_sync(~0u, U, o);
+  U *= nh;
+  const long long ctas = U < gridDim.x ? U : gridDim.x;
+  if (blockIdx.x >= ctas) return;
+  const long long u0 = blockIdx.x * U / ctas, u1 = (blockIdx.x + 1) * U / ctas;
+  Cursor ci;
+  {
+    long long rem = u0;
+    int b = 0;
+    for (int base = 0; base < a.B; base += 32) {
+      Span s = {0, 0};
+      if (base + lane < a.B) s = span_of(a, base + lane);
+      const long long mine = (long long)s.tiles() * nh;
+      long long incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(~0u, incl, o);
+        if (lane >= o) incl += v;
+      }
+      const uint32_t over = __ballot_sync(~0u, incl > rem);
+      if (over) {
+        const int src = __ffs(over) - 1;
+        rem -= __shfl_sync(~0u, incl - mine, src);
+        b = base + src;
+        break;
+      }
+      rem -= __shfl_sync(~0u, incl, 31);
+    }
+    ci.b = b;
+    ci.s = span_of(a, b);
+    ci.nt = ci.s.tiles();
+    ci.h = (int)(rem / ci.nt);
+    ci.tile = (int)(rem % ci.nt);
+  }
+  Cursor cc = ci;  // ci issues loads ahead of cc, which computes
+
+  const uint32_t base = ptx::smem_u32(ring) + w * R::WARP;
+  const int nch = a.c.D * R::ES / 16;
+  // the page of this lane's token of the tile that is issued next
+  auto page_of = [&](const Cursor& k) {
+    const int rel = k.tile * kTile + w * kTok + (lane & 15);
+    if (k.b >= a.B || rel >= k.s.n) return -1;
+    return a.page_table[(int64_t)k.b * a.table_ld + (k.s.start + rel) / a.c.page_size];
+  };
+  int page = page_of(ci);
+  long long ui = u0;
+  auto issue = [&](int stage) {
+    if (ui < u1) {
+      const int rel = ci.tile * kTile + w * kTok + (lane & 15);
+      const int pos = ci.s.start + rel;
+      bool ok = rel < ci.s.n;
+      if (ok && (page < 0 || page >= a.c.n_pages)) {
+        set_status(a.status, MOE_ERR_DEVICE);
+        ok = false;
+      }
+      const int64_t off = ok ? (int64_t)page * a.c.page_stride +
+                                   (int64_t)(ci.h / a.nhb) * a.c.head_stride +
+                                   (int64_t)(pos % a.c.page_size) * a.c.token_stride
+                             : 0;
+      const uint32_t mask = __ballot_sync(~0u, ok) & 0xffff;
+      if (lane == 0) valid[w][stage] = mask;
+      const uint32_t kd = base + stage * R::STAGE, vd = kd + kTok * RB;
+#pragma unroll
+      for (int i = 0; i < CPR / 2; ++i) {
+        const int idx = i * 32 + lane, row = idx / CPR, ch = idx % CPR;
+        const int64_t o = __shfl_sync(~0u, off, row) * R::ES + ch * 16;
+        const bool v = ((mask >> row) & 1) && ch < nch;
+        const uint32_t d = swz<RB>(row, ch);
+        cp_async16(kd + d, (const uint8_t*)a.c.k_pages + (v ? o : 0), v ? 16 : 0);
+        cp_async16(vd + d, (const uint8_t*)a.c.v_pages + (v ? o : 0), v ? 16 : 0);
+      }
+      ++ui;
+      if (ui < u1) {
+        ci.next(a, nh);
+        page = page_of(ci);
+      }
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) issue(i);
+
+  uint32_t qa[KS][2 * RH];
+  float acc[NT][4], m[RH], l[RH], sc[RH];
+  auto begin_item = [&]() {
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+    const int kvh = cc.h / a.nhb, hb = cc.h % a.nhb;
+    const float ks = KV == MOE_DT_E4M3 && a.c.k_scale ? a.c.k_scale[kvh] : 1.f;
+#pragma unroll
+    for (int r = 0; r < RH; ++r) {
+      m[r] = __int_as_float(0xff800000);
+      l[r] = 0.f;
+      const int row = hb * ROWS + r * 8 + g;
+      const bool on = row < a.G;
+      const uint16_t* q =
+          (const uint16_t*)a.q + cc.b * a.q_row + (int64_t)(kvh * a.G + (on ? row : 0)) * a.q_head;
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        uint32_t x = 0, y = 0;
+        if (on && s * 16 < a.c.D) {
+          if constexpr (KV == MOE_DT_E4M3) {
+            const uint2 v = *(const uint2*)(q + s * 16 + c4 * 4);
+            x = v.x, y = v.y;
+          } else {
+            x = *(const uint32_t*)(q + s * 16 + c4 * 2);
+            y = *(const uint32_t*)(q + s * 16 + 8 + c4 * 2);
+          }
+        }
+        qa[s][r] = x;
+        qa[s][RH + r] = y;
+      }
+      float back = 1.f;
+      if (KV == MOE_DT_E4M3 && a.q_bf16) {
+        // keys are held in f16 (exact for E4M3), so a bf16 query goes to f16
+        // under a power of two that brings its largest value to [2^14, 2^15):
+        // exact but for values 2^-29 below that
+        float top = 0.f;
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t v = qa[s][j * RH + r];
+            top = fmaxf(top, fmaxf(fabsf(bf16_lo(v)), fabsf(bf16_hi(v))));
+          }
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+        const int e = (int)(__float_as_uint(top) >> 23) - 127;
+        const int up = e == 128 || top == 0.f ? 0 : min(14 - e, 100);
+        const float f = __uint_as_float((uint32_t)(127 + up) << 23);
+        back = __uint_as_float((uint32_t)(127 - up) << 23);
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t v = qa[s][j * RH + r];
+            qa[s][j * RH + r] = pack_f16(bf16_lo(v) * f, bf16_hi(v) * f);
+          }
+      }
+      sc[r] = a.scale * ks * back;
+    }
+  };
+
+  // all warps' results of an item: to the output, or a part of it to the
+  // workspace; t0, t1: the tiles of the item that this run covered
+  auto end_item = [&](long long first_u, int t0, int t1) {
+    const int kvh = cc.h / a.nhb, hb = cc.h % a.nhb;
+#pragma unroll
+    for (int r = 0; r < RH; ++r) {
+      l[r] += __shfl_xor_sync(~0u, l[r], 1);
+      l[r] += __shfl_xor_sync(~0u, l[r], 2);
+      if (c4 == 0) ml[w][r * 8 + g] = make_float2(m[r], l[r]);
+    }
+    __syncthreads();
+    auto top_of = [&](int row) {
+      float M = ml[0][row].x;
+#pragma unroll
+      for (int i = 1; i < kWarps; ++i) M = fmaxf(M, ml[i][row].x);
+      return M;
+    };
+    auto zero_if_empty = [](float M) { return M == __int_as_float(0xff800000) ? 0.f : M; };
+    float f[RH];
+#pragma unroll
+    for (int r = 0; r < RH; ++r) f[r] = exp2_approx(m[r] - zero_if_empty(top_of(r * 8 + g)));
+    // value (n tile i, row half r, column j) of this lane
+    auto value = [&](int i, int r, int j) {
+      if constexpr (RH == 1) return (acc[i][j] + acc[i][2 + j]) * f[0];
+      else return acc[i][2 * r + j] * f[r];
+    };
+    auto slot = [&](int i, int r, int j) { return ((i * RH + r) * 2 + j) * 32 + lane; };
+    constexpr int ROUNDS = RH == 1 ? 2 : 4;  // warps add into the slices one after another
+    float* mine = mb + (RH == 1 ? (w & 1) * ROWS * DP : 0);
+    const int turn = RH == 1 ? 1 - (w >> 1) : kWarps - 1 - w;
+#pragma unroll
+    for (int k = 0; k < ROUNDS; ++k) {
+      if (turn == k) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int r = 0; r < RH; ++r)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              float* p = mine + slot(i, r, j);
+              *p = k == 0 ? value(i, r, j) : *p + value(i, r, j);
+            }
+      }
+      __syncthreads();
+    }
+    if (RH == 1) {
+      for (int i = threadIdx.x; i < ROWS * DP / 4; i += blockDim.x) {
+        float4 x = ((float4*)mb)[i];
+        const float4 y = ((float4*)(mb + ROWS * DP))[i];
+        x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+        ((float4*)mb)[i] = x;
+      }
+      __syncthreads();
+    }
+    // mb: the item's sums relative to M; (M, L) of each row
+    float M = 0.f, L = 0.f;
+    if (threadIdx.x < ROWS) {
+      M = top_of(threadIdx.x);
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i)
+        L += ml[i][threadIdx.x].y * exp2_approx(ml[i][threadIdx.x].x - zero_if_empty(M));
+    }
+    __syncthreads();
+    if (threadIdx.x < ROWS) ml[0][threadIdx.x] = make_float2(M, L);
+
+    bool write = t0 == 0 && t1 == cc.nt;
+    if (!write) {
+      // CTA c runs tiles [c U / ctas, (c + 1) U / ctas)
+      const int cs = (int)(((first_u + 1) * ctas - 1) / U);
+      const int ce = (int)(((first_u + cc.nt) * ctas - 1) / U);
+      const int np = ce - cs + 1;
+      auto part = [&](int p) { return a.parts + (size_t)(p == 0 ? 2 * cs + 1 : 2 * (cs + p)) * PART; };
+      float* to = part(blockIdx.x - cs);
+      for (int i = threadIdx.x; i < ROWS * DP / 4; i += blockDim.x)
+        ((float4*)to)[i] = ((float4*)mb)[i];
+      if (threadIdx.x < ROWS)
+        ((float2*)(to + ROWS * DP))[threadIdx.x] = make_float2(M, L);
+      __threadfence();
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        const unsigned done = atomicAdd(a.counters + cs, 1u);
+        is_last = done == (unsigned)np - 1;
+        if (is_last) a.counters[cs] = 0;
+      }
+      __syncthreads();
+      write = is_last;
+      if (write) {
+        __threadfence();
+        if (threadIdx.x < ROWS) {
+          M = __int_as_float(0xff800000);
+          for (int p = 0; p < np; ++p)
+            M = fmaxf(M, __ldcg((const float2*)(part(p) + ROWS * DP) + threadIdx.x).x);
+          L = 0.f;
+          for (int p = 0; p < np; ++p) {
+            const float2 v = __ldcg((const float2*)(part(p) + ROWS * DP) + threadIdx.x);
+            L += v.y * exp2_approx(v.x - zero_if_empty(M));
+          }
+          ml[0][threadIdx.x] = make_float2(M, L);
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < ROWS * DP / 4; i += blockDim.x) {
+          const int row = (i & 7) + 8 * ((i / 16) % RH);
+          const float Mr = zero_if_empty(ml[0][row].x);
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+          for (int p = 0; p < np; ++p) {
+            const float* from = part(p);
+            const float4 y = __ldcg((const float4*)from + i);
+            const float e = exp2_approx(__ldcg((const float2*)(from + ROWS * DP) + row).x - Mr);
+            x.x += y.x * e, x.y += y.y * e, x.z += y.z * e, x.w += y.w * e;
+          }
+          ((float4*)mb)[i] = x;
+        }
+      }
+    }
+    __syncthreads();
+    if (write) {
+      const float vs = KV == MOE_DT_E4M3 && a.c.v_scale ? a.c.v_scale[kvh] : 1.f;
+      for (int u = threadIdx.x; u < KS * ROWS; u += blockDim.x) {
+        const int row = u % ROWS, p = u / ROWS;  // 16 values of one head
+        const int head = hb * ROWS + row;
+        if (head >= a.G || p * 16 >= a.c.D) continue;
+        const float2 st = ml[0][row];
+        const float k = st.y == 0.f ? 0.f : vs / st.y;
+        float o[16];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float4 x =
+                *(const float4*)(mb + (((2 * p + i) * RH + (row >> 3)) * 2 + j) * 32 + (row & 7) * 4);
+            const float v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              // see the V fragments: with 8-bit values tile i holds the even or odd ones
+              const int d = KV == MOE_DT_E4M3 ? 4 * c + 2 * j + i : 8 * i + 2 * c + j;
+              o[d] = v[c] * k;
+            }
+          }
+        uint16_t* dst = (uint16_t*)a.out + cc.b * a.out_row +
+                        (int64_t)(kvh * a.G + head) * a.out_head + p * 16;
+        uint32_t pk[8];
+#pragma unroll
+        for (int d = 0; d < 8; ++d)
+          pk[d] = a.q_bf16 ? pack_bf16(o[2 * d], o[2 * d + 1]) : pack_f16(o[2 * d], o[2 * d + 1]);
+        ((uint4*)dst)[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+        ((uint4*)dst)[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+        if (p == 0 && a.lse)
+          a.lse[(int64_t)cc.b * a.Hq + kvh * a.G + head] =
+              (st.x + log2f(st.y)) * (1.f / kLog2e);
+      }
+    }
+    __syncthreads();
+  };
+
+  begin_item();
+  int t0 = cc.tile;
+  int stage = 0;
+  for (long long u = u0; u < u1; ++u) {
+    cp_async_wait<S - 2>();
+    __syncwarp();
+    {
+      const int to = stage == 0 ? S - 1 : stage - 1;
+      issue(to);
+    }
+    const uint32_t kd = base + stage * R::STAGE, vd = kd + kTok * RB;
+    const uint32_t mask = valid[w][stage];
+
+    float s[2][4] = {};
+    if constexpr (KV == MOE_DT_E4M3) {
+      const int row = (lane & 7) + ((lane >> 3) & 1) * 8;
+#pragma unroll
+      for (int k = 0; k < KS; k += 2) {
+        uint32_t r[4];
+        ldmatrix_x4(r, kd + swz<RB>(row, k + (lane >> 4)));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int kk = k + (i >> 1);
+          uint32_t qf[4];
+          qf[0] = qa[kk][0], qf[1] = RH == 2 ? qa[kk][RH - 1] : 0u;
+          qf[2] = qa[kk][RH], qf[3] = RH == 2 ? qa[kk][2 * RH - 1] : 0u;
+          mma16816<MT>(s[i & 1], qf, e4m3x2_to_f16x2(r[i] & 0xffff), e4m3x2_to_f16x2(r[i] >> 16));
+        }
+      }
+    } else {
+      const int row = (lane & 7) + (lane >> 4) * 8;
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        uint32_t r[4];
+        ldmatrix_x4(r, kd + swz<RB>(row, 2 * k + ((lane >> 3) & 1)));
+        uint32_t qf[4];
+        qf[0] = qa[k][0], qf[1] = RH == 2 ? qa[k][RH - 1] : 0u;
+        qf[2] = qa[k][RH], qf[3] = RH == 2 ? qa[k][2 * RH - 1] : 0u;
+        mma16816<MT>(s[0], qf, r[0], r[1]);
+        mma16816<MT>(s[1], qf, r[2], r[3]);
+      }
+    }
+
+    // scores in units of log2, running maximum and sum
+    float p[2][2 * RH];
+    bool grew = false;
+    float al[RH];
+#pragma unroll
+    for (int r = 0; r < RH; ++r) {
+      float top = m[r];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float v = s[i][2 * r + j] * sc[r];
+          if (a.softcap > 0.f) v = a.softcap * tanhf(v / a.softcap);
+          v = (mask >> (i * 8 + c4 * 2 + j)) & 1 ? v * kLog2e : __int_as_float(0xff800000);
+          p[i][2 * r + j] = v;
+          top = fmaxf(top, v);
+        }
+      top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+      const float z = top == __int_as_float(0xff800000) ? 0.f : top;
+      al[r] = exp2_approx(m[r] - z);
+      grew |= top != m[r];
+      m[r] = top;
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          p[i][2 * r + j] = exp2_approx(p[i][2 * r + j] - z);
+          sum += p[i][2 * r + j];
+        }
+      l[r] = l[r] * al[r] + sum;
+    }
+    if (__any_sync(~0u, grew)) {
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] *= al[RH == 1 ? 0 : j >> 1];
+    }
+    // P as the sum of two 16-bit numbers (hi + lo, 16 or 22 bits): rounding it
+    // once to bf16 would cost as much as the output's own rounding.  With up
+    // to 8 heads the lo parts ride in the tile's other 8 rows, at no cost.
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int r = 0; r < RH; ++r) {
+        const float x = p[i][2 * r], y = p[i][2 * r + 1];
+        const uint32_t h = pack2<MT>(x, y);
+        const uint32_t rest = pack2<MT>(x - lo2<MT>(h), y - hi2<MT>(h));
+        if constexpr (RH == 1) {
+          hi[2 * i] = h;
+          hi[2 * i + 1] = rest;
+        } else {
+          hi[2 * i + r] = h;
+          lo[2 * i + r] = rest;
+        }
+      }
+    const int row = (lane & 7) + ((lane >> 3) & 1) * 8;
+#pragma unroll
+    for (int k = 0; k < CPR; k += 2) {
+      uint32_t r[4];
+      ldmatrix_x4_trans(r, vd + swz<RB>(row, k + (lane >> 4)));
+      if constexpr (KV == MOE_DT_E4M3) {
+        // a 16-bit element holds values 2n, 2n + 1 of a token; a register two
+        // tokens' pairs.  Bytes 0, 2 (values 2n) feed one tile, 1, 3 the next.
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t x = __byte_perm(r[2 * i], 0, 0x3120), y = __byte_perm(r[2 * i + 1], 0, 0x3120);
+#pragma unroll
+          for (int o = 0; o < 2; ++o) {
+            const uint32_t b0 = e4m3x2_to_f16x2(o ? x >> 16 : x & 0xffff);
+            const uint32_t b1 = e4m3x2_to_f16x2(o ? y >> 16 : y & 0xffff);
+            mma16816<MT>(acc[2 * (k + i) + o], hi, b0, b1);
+            if constexpr (RH == 2) mma16816<MT>(acc[2 * (k + i) + o], lo, b0, b1);
+          }
+        }
+      } else {
+        mma16816<MT>(acc[k], hi, r[0], r[1]);
+        mma16816<MT>(acc[k + 1], hi, r[2], r[3]);
+        if constexpr (RH == 2) {
+          mma16816<MT>(acc[k], lo, r[0], r[1]);
+          mma16816<MT>(acc[k + 1], lo, r[2], r[3]);
+        }
+      }
+    }
+
+    stage = stage + 1 == S ? 0 : stage + 1;
+    const bool done = cc.tile + 1 == cc.nt;
+    if (done || u + 1 == u1) {
+      end_item(u - cc.tile, t0, cc.tile + 1);
+      if (u + 1 < u1) {
+        cc.next(a, nh);
+        begin_item();
+        t0 = 0;
+      }
+    } else {
+      cc.next(a, nh);
+    }
+  }
+  cp_async_wait<0>();
+}
+
+template <int KV, int DP, int RH>
+moe_status launch_attend(const AttendArgs& a, cudaStream_t s) {
+  constexpr int smem = Ring<KV, DP>::BYTES + (RH == 1 ? 2 : 1) * 8 * RH * DP * 4;
+  static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is raised
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return launch_status(cudaErrorUnknown);
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(ready.load(std::memory_order_relaxed) & bit)) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        k_attend<KV, DP, RH>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return launch_status(e);
+    ready.fetch_or(bit, std::memory_order_relaxed);
+  }
+  // no more CTAs than tiles there can be
+  const int64_t tiles = ((int64_t)a.max_pages * a.c.page_size + kTile - 1) / kTile;
+  const double most = (double)a.B * a.c.Hkv * a.nhb * (double)(tiles > 0 ? tiles : 1);
+  const int resident = smem > 113 * 1024 ? kSMs : kMaxCtas;
+  const int grid = most < resident ? (int)most : resident;
+  return launch_status(launch_pdl(k_attend<KV, DP, RH>, grid, kWarps * 32, smem, s, a));
+}
+
+template <int KV>
+moe_status pick_attend(const AttendArgs& a, cudaStream_t s) {
+  const int D = a.c.D;
+  if (a.G <= 8) {
+    if (D <= 64) return launch_attend<KV, 64, 1>(a, s);
+    if (D <= 128) return launch_attend<KV, 128, 1>(a, s);
+    return launch_attend<KV, 256, 1>(a, s);
+  }
+  if (D <= 64) return launch_attend<KV, 64, 2>(a, s);
+  if (D <= 128) return launch_attend<KV, 128, 2>(a, s);
+  return launch_attend<KV, 256, 2>(a, s);
+}
+
+bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+
+// the checks both calls share
+moe_status check_view(const kvcache_view& c, int dtype) {
+  if (c.Hkv <= 0 || c.D <= 0 || c.page_size <= 0 || c.n_pages < 0) return MOE_ERR_INVALID_ARG;
+  if (dtype != MOE_DT_BF16 && dtype != MOE_DT_F16) return MOE_ERR_UNSUPPORTED;
+  if (c.kv_type != dtype && c.kv_type != MOE_DT_E4M3) return MOE_ERR_UNSUPPORTED;
+  if (c.D % 16 || c.D > 256) return MOE_ERR_UNSUPPORTED;
+  if (!c.k_pages || !c.v_pages) return MOE_ERR_INVALID_ARG;
+  if (c.page_stride < 0 || c.head_stride < 0 || c.token_stride < 0) return MOE_ERR_INVALID_ARG;
+  const int unit = c.kv_type == MOE_DT_E4M3 ? 16 : 8;
+  if (c.page_stride % unit || c.head_stride % unit || c.token_stride % unit ||
+      !aligned16(c.k_pages) || !aligned16(c.v_pages))
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+bool rows_ok(const void* p, int64_t row, int64_t head) {
+  return aligned16(p) && row % 8 == 0 && head % 8 == 0;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+MOE_API moe_status kvcache_append(const kvcache_append_args* a, void* stream) {
+  if (!a || a->N < 0 || a->Hq < 0) return MOE_ERR_INVALID_ARG;
+  moe_status st = check_view(a->c, a->dtype);
+  if (st != MOE_OK) return st;
+  if (a->n_seqs < 0 || a->max_pages < 0) return MOE_ERR_INVALID_ARG;
+  if ((a->cos == nullptr) != (a->sin == nullptr)) return MOE_ERR_INVALID_ARG;
+  if (a->cos) {
+    if (a->rot <= 0 || a->rot > a->c.D || a->max_pos < 0) return MOE_ERR_INVALID_ARG;
+    if (a->rot % 16 || !aligned16(a->cos) || !aligned16(a->sin)) return MOE_ERR_UNSUPPORTED;
+  }
+  if (a->N == 0) return MOE_OK;
+  if (!a->k || !a->v || !a->pos || !a->page_table) return MOE_ERR_INVALID_ARG;
+  if (a->q && (!a->q_out || a->Hq == 0)) return MOE_ERR_INVALID_ARG;
+  if (!rows_ok(a->k, a->k_row, a->k_head) || !rows_ok(a->v, a->v_row, a->v_head) ||
+      (a->q && (!rows_ok(a->q, a->q_row, a->q_head) ||
+                !rows_ok(a->q_out, a->q_out_row, a->q_out_head))))
+    return MOE_ERR_UNSUPPORTED;
+  kvcache_append_args b = *a;
+  if (!b.q) b.Hq = 0;
+  if (!b.cos) b.rot = 0;
+  const int lanes = kAppendThreads / (b.c.D / 16);
+  const int heads = b.Hq + 2 * b.c.Hkv;
+  const dim3 grid(b.N, b.N < kSMs ? (heads + lanes - 1) / lanes : 1);
+  cudaStream_t s = (cudaStream_t)stream;
+  cudaError_t e;
+  if (b.dtype == MOE_DT_BF16)
+    e = b.c.kv_type == MOE_DT_E4M3
+            ? launch_pdl(k_append<MOE_DT_BF16, MOE_DT_E4M3>, grid, kAppendThreads, 0, s, b)
+            : launch_pdl(k_append<MOE_DT_BF16, MOE_DT_BF16>, grid, kAppendThreads, 0, s, b);
+  else
+    e = b.c.kv_type == MOE_DT_E4M3
+            ? launch_pdl(k_append<MOE_DT_F16, MOE_DT_E4M3>, grid, kAppendThreads, 0, s, b)
+            : launch_pdl(k_append<MOE_DT_F16, MOE_DT_F16>, grid, kAppendThreads, 0, s, b);
+  return launch_status(e);
+}
+
+MOE_API size_t kvcache_attend_workspace_bytes(int Hq, int Hkv, int D) {
+  if (Hq <= 0 || Hkv <= 0 || Hq % Hkv || D <= 0 || D > 256) return 0;
+  const size_t rows = Hq / Hkv <= 8 ? 8 : 16, dp = D <= 64 ? 64 : D <= 128 ? 128 : 256;
+  return kCtlBytes + (size_t)kMaxCtas * 2 * rows * (dp + 2) * sizeof(float);
+}
+
+MOE_API moe_status kvcache_attend(const kvcache_attend_args* a, void* stream) {
+  if (!a || a->B < 0 || a->Hq <= 0) return MOE_ERR_INVALID_ARG;
+  moe_status st = check_view(a->c, a->dtype);
+  if (st != MOE_OK) return st;
+  if (a->Hq % a->c.Hkv) return MOE_ERR_UNSUPPORTED;
+  if (a->max_pages < 0 || a->window < 0 || !(a->softcap >= 0.f)) return MOE_ERR_INVALID_ARG;
+  if (a->B == 0) return MOE_OK;
+  if (!a->q || !a->out || !a->page_table || !a->seq_lens || !a->workspace)
+    return MOE_ERR_INVALID_ARG;
+  if (a->workspace_bytes < kvcache_attend_workspace_bytes(a->Hq, a->c.Hkv, a->c.D))
+    return MOE_ERR_INVALID_ARG;
+  if (!rows_ok(a->q, a->q_row, a->q_head) || !rows_ok(a->out, a->out_row, a->out_head) ||
+      !aligned16(a->workspace))
+    return MOE_ERR_UNSUPPORTED;
+  AttendArgs k;
+  k.c = a->c;
+  k.B = a->B, k.Hq = a->Hq, k.G = a->Hq / a->c.Hkv;
+  k.nhb = k.G <= 8 ? 1 : (k.G + 15) / 16;
+  k.q = a->q, k.out = a->out, k.lse = a->lse;
+  k.q_row = a->q_row, k.q_head = a->q_head, k.out_row = a->out_row, k.out_head = a->out_head;
+  k.table_ld = a->table_ld, k.page_table = a->page_table, k.seq_lens = a->seq_lens;
+  k.max_pages = a->max_pages, k.window = a->window, k.q_bf16 = a->dtype == MOE_DT_BF16;
+  k.scale = a->scale, k.softcap = a->softcap;
+  k.counters = (unsigned*)a->workspace;
+  k.parts = (float*)((uint8_t*)a->workspace + kCtlBytes);
+  k.status = a->status;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (a->c.kv_type == MOE_DT_E4M3) return pick_attend<MOE_DT_E4M3>(k, s);
+  if (a->c.kv_type == MOE_DT_BF16) return pick_attend<MOE_DT_BF16>(k, s);
+  return pick_attend<MOE_DT_F16>(k, s);
+}

@@ -20,6 +20,7 @@ MOE_MODE_DECODE, MOE_MODE_PREFILL = 0, 1
 MOE_STAGE_GATE_UP, MOE_STAGE_DOWN, MOE_STAGE_ALL = 1, 2, 3
 
 vp, i32, u64, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint64, ctypes.c_size_t
+i64, f32 = ctypes.c_int64, ctypes.c_float
 
 
 class MoeError(RuntimeError):
@@ -64,6 +65,45 @@ class moe_layer_desc(ctypes.Structure):
                 ("skip_tau", ctypes.c_float)]
 
 
+class moe_block_norm_args(ctypes.Structure):
+    _fields_ = [("T", i32), ("H", i32), ("kind", i32), ("stream_type", i32), ("branch_type", i32),
+                ("weight_type", i32), ("x", vp), ("ldx", i64), ("y", vp), ("ldy", i64),
+                ("gate", vp), ("gate_row", i64), ("gate_col", i64), ("gate_act", i32),
+                ("post_norm", i32), ("w_post", vp), ("b_post", vp), ("w_pre", vp), ("b_pre", vp),
+                ("res_scale", f32), ("branch_scale", f32), ("eps", f32), ("w_offset", f32),
+                ("r", vp), ("ldr", i64), ("h", vp), ("ldh", i64)]
+
+
+class kvcache_view(ctypes.Structure):
+    _fields_ = [("k_pages", vp), ("v_pages", vp), ("page_stride", i64), ("head_stride", i64),
+                ("token_stride", i64), ("n_pages", i32), ("page_size", i32), ("Hkv", i32),
+                ("D", i32), ("kv_type", i32), ("k_scale", vp), ("v_scale", vp)]
+
+
+class kvcache_append_args(ctypes.Structure):
+    _fields_ = [("c", kvcache_view), ("N", i32), ("Hq", i32), ("dtype", i32),
+                ("k", vp), ("k_row", i64), ("k_head", i64), ("v", vp), ("v_row", i64),
+                ("v_head", i64), ("q", vp), ("q_row", i64), ("q_head", i64), ("q_out", vp),
+                ("q_out_row", i64), ("q_out_head", i64), ("seq", vp), ("pos", vp),
+                ("page_table", vp), ("table_ld", i64), ("n_seqs", i32), ("max_pages", i32),
+                ("cos", vp), ("sin", vp), ("rot", i32), ("max_pos", i32), ("interleaved", i32),
+                ("status", vp)]
+
+
+class kvcache_attend_args(ctypes.Structure):
+    _fields_ = [("c", kvcache_view), ("B", i32), ("Hq", i32), ("dtype", i32),
+                ("q", vp), ("q_row", i64), ("q_head", i64), ("out", vp), ("out_row", i64),
+                ("out_head", i64), ("lse", vp), ("page_table", vp), ("table_ld", i64),
+                ("max_pages", i32), ("seq_lens", vp), ("scale", f32), ("softcap", f32),
+                ("window", i32), ("workspace", vp), ("workspace_bytes", sz), ("status", vp)]
+
+
+class moe_w4_linear_args(ctypes.Structure):
+    _fields_ = [("T", i32), ("N", i32), ("K", i32), ("group", i32), ("dtype", i32),
+                ("format", i32), ("x", vp), ("ldx", i64), ("codes", vp), ("scales", vp),
+                ("zeros", vp), ("bias", vp), ("y", vp), ("ldy", i64)]
+
+
 # every function declared in include/moe.h: name -> (restype, argtypes)
 SIGNATURES = {
     "moe_status_string": (ctypes.c_char_p, [i32]),
@@ -96,6 +136,11 @@ SIGNATURES = {
     "moe_layer_debug_prefill": (i32, [vp, vp, vp, vp]),
     "moe_layer_set_timing": (i32, [vp, vp, i32]),
     "moe_read_device_status": (i32, [vp, vp, ctypes.POINTER(ctypes.c_int32)]),
+    "moe_block_norm": (i32, [ctypes.POINTER(moe_block_norm_args), vp]),
+    "kvcache_append": (i32, [ctypes.POINTER(kvcache_append_args), vp]),
+    "kvcache_attend_workspace_bytes": (sz, [i32, i32, i32]),
+    "kvcache_attend": (i32, [ctypes.POINTER(kvcache_attend_args), vp]),
+    "moe_w4_linear": (i32, [ctypes.POINTER(moe_w4_linear_args), vp]),
 }
 
 _lib = None
@@ -285,3 +330,30 @@ def moe_read_device_status(layer: int, stream: int = 0) -> int:
     v = ctypes.c_int32(0)
     _ck("moe_read_device_status", lib().moe_read_device_status(layer, stream, ctypes.byref(v)))
     return v.value
+
+
+# ------------------------------------------------------------- decode block
+MOE_DT_BF16, MOE_DT_F32, MOE_DT_F16, MOE_DT_E4M3 = 0, 1, 2, 3
+MOE_NORM_RMS, MOE_NORM_LAYER = 0, 1
+MOE_GATE_NONE, MOE_GATE_SIGMOID = 0, 1
+MOE_W4_U4, MOE_W4_E2M1 = 0, 1
+
+
+def moe_block_norm(args: moe_block_norm_args, stream: int = 0) -> None:
+    _ck("moe_block_norm", lib().moe_block_norm(ctypes.byref(args), stream))
+
+
+def kvcache_append(args: kvcache_append_args, stream: int = 0) -> None:
+    _ck("kvcache_append", lib().kvcache_append(ctypes.byref(args), stream))
+
+
+def kvcache_attend_workspace_bytes(Hq: int, Hkv: int, D: int) -> int:
+    return int(lib().kvcache_attend_workspace_bytes(Hq, Hkv, D))
+
+
+def kvcache_attend(args: kvcache_attend_args, stream: int = 0) -> None:
+    _ck("kvcache_attend", lib().kvcache_attend(ctypes.byref(args), stream))
+
+
+def moe_w4_linear(args: moe_w4_linear_args, stream: int = 0) -> None:
+    _ck("moe_w4_linear", lib().moe_w4_linear(ctypes.byref(args), stream))
