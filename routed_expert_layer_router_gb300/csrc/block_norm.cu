@@ -6,6 +6,9 @@
 // row and keeps it in registers as fp32 (kVec * VPT values a thread), so the
 // statistics cost no second read; a layer norm's variance is taken around the
 // mean from the registers.  Weights and channel gates come through L1 / L2.
+#include <atomic>
+#include <type_traits>
+
 #include "elem.cuh"
 
 namespace moe {
@@ -22,14 +25,25 @@ struct NormArgs {
 template <int DT, int VEC>
 __device__ __forceinline__ void load(const void* p, int64_t i, float (&v)[VEC]) {
   const typename Elem<DT>::T* q = (const typename Elem<DT>::T*)p + i;
-  if constexpr (VEC == 1) v[0] = to_f32<DT>(*q);
-  else load8<DT>(q, v);
+  if constexpr (VEC == 8) {
+    load8<DT>(q, v);
+  } else if constexpr (VEC == 1) {
+    v[0] = to_f32<DT>(*q);
+  } else if constexpr (DT == MOE_DT_F32) {
+    const float2 u = *(const float2*)q;
+    v[0] = u.x, v[1] = u.y;
+  } else {
+    const uint32_t u = *(const uint32_t*)q;
+    v[0] = lo2<DT>(u), v[1] = hi2<DT>(u);
+  }
 }
 template <int DT, int VEC>
 __device__ __forceinline__ void store(void* p, int64_t i, const float (&v)[VEC]) {
   typename Elem<DT>::T* q = (typename Elem<DT>::T*)p + i;
-  if constexpr (VEC == 1) *q = from_f32<DT>(v[0]);
-  else store8<DT>(q, v);
+  if constexpr (VEC == 8) store8<DT>(q, v);
+  else if constexpr (VEC == 1) *q = from_f32<DT>(v[0]);
+  else if constexpr (DT == MOE_DT_F32) *(float2*)q = make_float2(v[0], v[1]);
+  else *(uint32_t*)q = pack2<DT>(v[0], v[1]);
 }
 
 // sum over the CTA, the same bits in every thread; `slot` alternates between
@@ -46,8 +60,9 @@ __device__ __forceinline__ float block_sum(float v, float (*part)[32], int& slot
   return v;
 }
 
-template <int RT, int BT, int VEC, int VPT>
-__global__ void __launch_bounds__(1024) k_block_norm(NormArgs a) {
+// VEC values an access, VPT accesses a thread, at most MAXT threads a row
+template <int RT, int BT, int VEC, int VPT, int MAXT>
+__global__ void __launch_bounds__(MAXT) k_block_norm(NormArgs a) {
   __shared__ float part[2][32];
   int slot = 0;
   const int H = a.H, step = blockDim.x * VEC;
@@ -163,22 +178,196 @@ __global__ void __launch_bounds__(1024) k_block_norm(NormArgs a) {
   }
 }
 
-template <int RT, int BT, int VEC, int VPT>
-cudaError_t launch(const NormArgs& a, int threads, cudaStream_t s) {
-  return launch_pdl(k_block_norm<RT, BT, VEC, VPT>, a.T, threads, 0, s, a);
+// Many rows: a CTA stays and walks rows t, t + grid, ...  A thread owns 8 values
+// of every row, so the weights (and a channel gate) stay in its registers, and
+// its share of the next rows' x, y (and gate) comes ahead into shared memory by
+// cp.async: a thread reads back only what it copied itself, so the ring needs
+// no barrier, and memory stays busy while a row's two reductions run.
+template <int RT, int BT, int MAXT>
+__global__ void __launch_bounds__(MAXT) k_block_norm_rows(NormArgs a, int stages) {
+  constexpr int XV = RT == MOE_DT_F32 ? 2 : 1, BV = BT == MOE_DT_F32 ? 2 : 1;  // 16-byte pieces
+  extern __shared__ __align__(16) uint4 ring[];
+  __shared__ float part[2][32];
+  int slot = 0;
+  const int i = threadIdx.x * 8, nthr = blockDim.x;
+  const bool in = i < a.H;
+  const bool full_gate = a.gate && a.gate_col && a.gate_row;
+  const int planes = XV + (a.y ? BV : 0) + (full_gate ? BV : 0);
+  const float inv_h = 1.f / (float)a.H;
+  pdl_wait();
+  pdl_launch_dependents();
+
+  const uint32_t mine = (uint32_t)__cvta_generic_to_shared(ring) + threadIdx.x * 16;
+  auto issue = [&](int64_t t, int stage) {
+    if (t < a.T && in) {
+      uint32_t d = mine + stage * planes * nthr * 16;
+      auto copy = [&](const void* p, int n) {
+        for (int k = 0; k < n; ++k, d += nthr * 16) cp_async16(d, (const uint8_t*)p + k * 16, 16);
+      };
+      copy((const typename Elem<RT>::T*)a.x + t * a.ldx + i, XV);
+      if (a.y) copy((const typename Elem<BT>::T*)a.y + t * a.ldy + i, BV);
+      if (full_gate) copy((const typename Elem<BT>::T*)a.gate + t * a.gate_row + i, BV);
+    }
+    cp_async_commit();
+  };
+  const int64_t step = gridDim.x;
+  for (int k = 0; k < stages - 1; ++k) issue(blockIdx.x + k * step, k);
+
+  float w_post[8], w_pre[8], cg[8];
+  auto weights = [&](const void* w, float (&v)[8], float off) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = 1.f;
+    if (w && in) {
+      if (a.w16) load<BT, 8>(w, i, v);
+      else load<MOE_DT_F32, 8>(w, i, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] += off;
+    }
+  };
+  auto gated = [&](float v) {
+    return a.branch_scale * (a.gate_act == MOE_GATE_SIGMOID ? 1.f / (1.f + expf(-v)) : v);
+  };
+  weights(a.w_post, w_post, a.w_offset);
+  weights(a.w_pre, w_pre, a.w_offset);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) cg[j] = a.branch_scale;
+  if (a.gate && a.gate_col && !a.gate_row && in) {
+    load<BT, 8>(a.gate, i, cg);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) cg[j] = gated(cg[j]);
+  }
+
+  auto norm = [&](float (&v)[8], const float (&w)[8], const void* c) {
+    float mean = 0.f;
+    if (a.kind == MOE_NORM_LAYER) {
+      float s = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s += v[j];
+      mean = block_sum(in ? s : 0.f, part, slot) * inv_h;
+    }
+    float s = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v[j] -= mean;
+      s += v[j] * v[j];
+    }
+    const float rs = rsqrtf(block_sum(in ? s : 0.f, part, slot) * inv_h + a.eps);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] *= rs * w[j];
+    if (c && in) {
+      float u[8];
+      if (a.w16) load<BT, 8>(c, i, u);
+      else load<MOE_DT_F32, 8>(c, i, u);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] += u[j];
+    }
+  };
+
+  int stage = 0;
+  for (int64_t t = blockIdx.x; t < a.T; t += step) {
+    // the oldest group is this row's; an empty group keeps the count at the end
+    if (stages == 2) cp_async_wait<0>();
+    else if (stages == 3) cp_async_wait<1>();
+    else if (stages == 4) cp_async_wait<2>();
+    else cp_async_wait<3>();
+    float r[8] = {}, b[8] = {}, g[8];
+    const uint4* p = ring + stage * planes * nthr + threadIdx.x;
+    auto take = [&](auto dt, float (&v)[8]) {
+      constexpr int DT = decltype(dt)::value;
+      uint4 q[2];
+      q[0] = p[0];
+      if constexpr (DT == MOE_DT_F32) q[1] = p[nthr];
+      load8<DT>(q, v);
+      p += (DT == MOE_DT_F32 ? 2 : 1) * nthr;
+    };
+    if (in) {
+      take(std::integral_constant<int, RT>(), r);
+      if (a.y) take(std::integral_constant<int, BT>(), b);
+    }
+    if (full_gate && in) {
+      take(std::integral_constant<int, BT>(), g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) g[j] = gated(g[j]);
+    } else if (a.gate && !a.gate_col) {
+      float one[1];
+      load<BT, 1>(a.gate, t * a.gate_row, one);
+      one[0] = gated(one[0]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) g[j] = one[0];
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) g[j] = cg[j];
+    }
+    issue(t + (stages - 1) * step, stage == 0 ? stages - 1 : stage - 1);
+    stage = stage + 1 == stages ? 0 : stage + 1;
+    if (a.post_norm) norm(b, w_post, a.b_post);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r[j] = a.res_scale * r[j] + g[j] * b[j];
+    if (a.r && in) store<RT, 8>(a.r, t * a.ldr + i, r);
+    if (a.h) {
+      norm(r, w_pre, a.b_pre);
+      if (in) store<BT, 8>(a.h, t * a.ldh + i, r);
+    }
+  }
+  cp_async_wait<0>();
 }
 
-template <int RT, int BT>
-cudaError_t dispatch(const NormArgs& a, bool vec, cudaStream_t s) {
-  const int per = vec ? 8 : 1, units = (a.H + per - 1) / per;
-  auto threads = [&](int vpt) { return ((units + vpt - 1) / vpt + 31) / 32 * 32; };
-  if (vec) {
-    if (threads(1) <= 1024) return launch<RT, BT, 8, 1>(a, threads(1), s);
-    if (threads(2) <= 1024) return launch<RT, BT, 8, 2>(a, threads(2), s);
-    return launch<RT, BT, 8, 4>(a, threads(4), s);
+template <int RT, int BT, int MAXT>
+cudaError_t launch_rows(const NormArgs& a, cudaStream_t s) {
+  auto* kern = k_block_norm_rows<RT, BT, MAXT>;
+  static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is raised
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  constexpr int kMost = 224 * 1024;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(ready.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_relaxed);
   }
-  if (threads(4) <= 1024) return launch<RT, BT, 1, 4>(a, threads(4), s);
-  return launch<RT, BT, 1, 32>(a, threads(32), s);
+  const int threads = ((a.H + 7) / 8 + 31) / 32 * 32;
+  const int planes = (RT == MOE_DT_F32 ? 2 : 1) +
+                     (BT == MOE_DT_F32 ? 2 : 1) *
+                         ((a.y ? 1 : 0) + (a.gate && a.gate_col && a.gate_row ? 1 : 0));
+  const int row = planes * threads * 16;
+  // registers allow 64K / (threads * (64 or 80)) rows an SM; the ring gets as
+  // deep as shared memory then allows, 5 at most
+  int per_sm = 65536 / (threads * (MAXT <= 768 ? 80 : 64));
+  if (per_sm > 24) per_sm = 24;
+  int stages = kMost / per_sm / row;
+  stages = stages > 5 ? 5 : stages < 2 ? 2 : stages;
+  while (per_sm > 1 && per_sm * (stages * row + 1280) > 227 * 1024) --per_sm;
+  const int grid = a.T < per_sm * kSMs ? a.T : per_sm * kSMs;
+  return launch_pdl(kern, grid, threads, (size_t)stages * row, s, a, stages);
+}
+
+template <int RT, int BT, int VEC, int VPT, int MAXT>
+cudaError_t launch(const NormArgs& a, cudaStream_t s) {
+  const int threads = ((a.H + VEC * VPT - 1) / (VEC * VPT) + 31) / 32 * 32;
+  return launch_pdl(k_block_norm<RT, BT, VEC, VPT, MAXT>, a.T, threads, 0, s, a);
+}
+
+// Few rows: one access a thread, so that a row's loads leave together (the
+// call's latency).  More than the GPU holds at once: the kernel that stays.
+template <int RT, int BT>
+cudaError_t dispatch(const NormArgs& a, int vec, cudaStream_t s) {
+  const int H = a.H;
+  if (vec == 8) {
+    if (a.T > 2 * kSMs && H <= 8 * 1024)
+      return H <= 8 * 768 ? launch_rows<RT, BT, 768>(a, s) : launch_rows<RT, BT, 1024>(a, s);
+    if (H <= 8 * 1024) return launch<RT, BT, 8, 1, 1024>(a, s);
+    if (H <= 8 * 2 * 1024) return launch<RT, BT, 8, 2, 1024>(a, s);
+    return launch<RT, BT, 8, 4, 1024>(a, s);
+  }
+  if (vec == 2) {
+    if (H <= 2 * 2 * 1024) return launch<RT, BT, 2, 2, 1024>(a, s);
+    if (H <= 2 * 4 * 1024) return launch<RT, BT, 2, 4, 1024>(a, s);
+    return launch<RT, BT, 2, 16, 1024>(a, s);
+  }
+  if (H <= 4 * 1024) return launch<RT, BT, 1, 4, 1024>(a, s);
+  if (H <= 8 * 1024) return launch<RT, BT, 1, 8, 1024>(a, s);
+  return launch<RT, BT, 1, 32, 1024>(a, s);
 }
 
 }  // namespace
@@ -215,15 +404,20 @@ MOE_API moe_status moe_block_norm(const moe_block_norm_args* a, void* stream) {
   k.res_scale = a->res_scale, k.branch_scale = a->branch_scale;
   k.eps = a->eps, k.w_offset = a->w_offset;
 
-  // 16-byte accesses of 8 values where every row that is read or written
-  // allows them; value by value otherwise
-  auto aligned = [](const void* p, int64_t ld) {
-    return !p || (((uintptr_t)p & 15) == 0 && ld % 8 == 0);
+  // accesses of 8 values (16 or 32 bytes), of 2, or value by value: what the
+  // alignment of every row that is read or written allows
+  auto vec_ok = [&](int n) {
+    auto ok = [n](const void* p, int64_t ld, int type) {
+      const int bytes = n * (type == MOE_DT_F32 ? 4 : 2);
+      return !p || ((uintptr_t)p % (bytes < 16 ? bytes : 16) == 0 && ld % n == 0);
+    };
+    return a->H % n == 0 && ok(a->x, a->ldx, RT) && ok(a->y, a->ldy, BT) &&
+           ok(a->r, a->ldr, RT) && ok(a->h, a->ldh, BT) &&
+           ok(a->w_post, 0, a->weight_type) && ok(a->b_post, 0, a->weight_type) &&
+           ok(a->w_pre, 0, a->weight_type) && ok(a->b_pre, 0, a->weight_type) &&
+           (!a->gate || a->gate_col == 0 || ok(a->gate, a->gate_row, BT));
   };
-  const bool vec = a->H % 8 == 0 && aligned(a->x, a->ldx) && aligned(a->y, a->ldy) &&
-                   aligned(a->r, a->ldr) && aligned(a->h, a->ldh) && aligned(a->w_post, 0) &&
-                   aligned(a->b_post, 0) && aligned(a->w_pre, 0) && aligned(a->b_pre, 0) &&
-                   (!a->gate || a->gate_col == 0 || aligned(a->gate, a->gate_row));
+  const int vec = vec_ok(8) ? 8 : vec_ok(2) ? 2 : 1;
   cudaStream_t s = (cudaStream_t)stream;
   cudaError_t e;
   if (RT == MOE_DT_BF16) e = dispatch<MOE_DT_BF16, MOE_DT_BF16>(k, vec, s);

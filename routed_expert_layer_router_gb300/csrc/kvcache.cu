@@ -31,18 +31,6 @@ __global__ void __launch_bounds__(kAppendThreads) k_append(kvcache_append_args a
 
   const int pos = a.pos[n];
   const int seq = a.seq ? a.seq[n] : n;
-  // token's place: page id and slot, or -1
-  int page = -1, at = 0;
-  if (pos >= 0) {
-    const int col = pos / a.c.page_size;
-    at = pos - col * a.c.page_size;
-    if (seq >= 0 && seq < a.n_seqs && col < a.max_pages && (!a.cos || pos < a.max_pos)) {
-      page = a.page_table[(int64_t)seq * a.table_ld + col];
-      if (page < 0 || page >= a.c.n_pages) page = -1;
-    }
-    if (page < 0 && threadIdx.x == 0) set_status(a.status, MOE_ERR_DEVICE);
-  }
-  const bool live = page >= 0;
 
   // d0, d1: where this thread's two runs of 8 values start; with rotation of
   // halves a run and its partner rot/2 further on, else 16 values in a row
@@ -51,25 +39,53 @@ __global__ void __launch_bounds__(kAppendThreads) k_append(kvcache_append_args a
   const bool apart = turn && !a.interleaved;
   const int d0 = apart ? it * 8 : it * 16;
   const int d1 = apart ? d0 + half : d0 + 8;
+
+  // a head's 16 values, as they lie in memory
+  struct Head {
+    uint4 u, w;
+  };
+  auto fetch = [&](int h) {
+    const E* src = h < a.Hq         ? (const E*)a.q + n * a.q_row + h * a.q_head
+                   : h < a.Hq + Hkv ? (const E*)a.k + n * a.k_row + (h - a.Hq) * a.k_head
+                                    : (const E*)a.v + n * a.v_row + (h - a.Hq - Hkv) * a.v_head;
+    return Head{*(const uint4*)(src + d0), *(const uint4*)(src + d1)};
+  };
+  // the first two heads' loads leave before the token's place is known
+  const int step = gridDim.y * lanes;
+  int h = blockIdx.y * lanes + hl;
+  Head next[2] = {};
+  if (h < heads) next[0] = fetch(h);
+  if (h + step < heads) next[1] = fetch(h + step);
+
+  // token's place: page id and slot, or -1
+  int page = -1, at = 0;
   float cs[8], sn[8];
-  if (turn && live) {
-    load8<MOE_DT_F32>(a.cos + (int64_t)pos * half + it * 8, cs);
-    load8<MOE_DT_F32>(a.sin + (int64_t)pos * half + it * 8, sn);
+  if (pos >= 0) {
+    const int col = pos / a.c.page_size;
+    at = pos - col * a.c.page_size;
+    if (seq >= 0 && seq < a.n_seqs && col < a.max_pages && (!a.cos || pos < a.max_pos)) {
+      page = a.page_table[(int64_t)seq * a.table_ld + col];
+      if (turn) {
+        load8<MOE_DT_F32>(a.cos + (int64_t)pos * half + it * 8, cs);
+        load8<MOE_DT_F32>(a.sin + (int64_t)pos * half + it * 8, sn);
+      }
+      if (page < 0 || page >= a.c.n_pages) page = -1;
+    }
+    if (page < 0 && threadIdx.x == 0) set_status(a.status, MOE_ERR_DEVICE);
   }
+  const bool live = page >= 0;
   const int64_t base = (int64_t)page * a.c.page_stride + (int64_t)at * a.c.token_stride;
 
-  const int first = blockIdx.y * lanes + hl;
-  for (int h = first; h < heads; h += gridDim.y * lanes) {
+  for (; h < heads; h += step) {
+    const Head cur = next[0];
+    next[0] = next[1];
+    if (h + 2 * step < heads) next[1] = fetch(h + 2 * step);
     const bool is_q = h < a.Hq, is_k = !is_q && h < a.Hq + Hkv;
     const int kh = is_q ? 0 : (is_k ? h - a.Hq : h - a.Hq - Hkv);
-    if (is_q && !a.q) continue;
     if (!is_q && !live) continue;
-    const E* src = is_q   ? (const E*)a.q + n * a.q_row + h * a.q_head
-                   : is_k ? (const E*)a.k + n * a.k_row + kh * a.k_head
-                          : (const E*)a.v + n * a.v_row + kh * a.v_head;
     float u[8], w[8];
-    load8<DT>(src + d0, u);
-    load8<DT>(src + d1, w);
+    load8<DT>(&cur.u, u);
+    load8<DT>(&cur.w, w);
     if (turn && live && (is_q || is_k)) {
       if (apart) {
 #pragma unroll
@@ -118,16 +134,16 @@ __global__ void __launch_bounds__(kAppendThreads) k_append(kvcache_append_args a
 
 // ------------------------------------------------------------------ attend
 // Bound by reading the cache once.  The sequences' tokens are cut into tiles
-// of 64; the tiles of all (sequence, kv head) items in a row are dealt to the
+// of 64 or 128; the tiles of all (sequence, kv head) items in a row are dealt to the
 // CTAs in equal contiguous runs, so a ragged batch and one long sequence fill
-// the GPU alike.  In a CTA each of 4 warps streams 16 tokens of a tile through
+// the GPU alike.  In a CTA each of 4 warps streams its 16 or 32 tokens of a tile through
 // its own ring of cp.async stages (no barrier between warps inside an item)
 // and keeps a running maximum, sum and output in registers.  The query heads
 // of a kv head are the rows of the matrix instructions, so K and V are read
 // once for all of them.  A run that covers an item writes its result; items
 // cut between CTAs leave their parts in the workspace, and the CTA that
 // finishes last adds them in run order (the same bits every time).
-constexpr int kWarps = 4, kTok = 16, kTile = kWarps * kTok;
+constexpr int kWarps = 4;
 constexpr int kMaxCtas = 2 * kSMs;
 constexpr size_t kCtlBytes = 4096;  // one counter a CTA
 static_assert(kMaxCtas * sizeof(unsigned) <= kCtlBytes, "counters");
@@ -137,7 +153,9 @@ template <int KV, int DP>
 struct Ring {
   static constexpr int ES = KV == MOE_DT_E4M3 ? 1 : 2;
   static constexpr int RB = DP * ES;             // bytes of a token's row
-  static constexpr int WARP = 2 * kTok * RB;     // one stage of one warp: K and V
+  static constexpr int TOK = RB <= 128 ? 32 : 16;  // tokens of a warp's stage: 8 KB where it can
+  static constexpr int TILE = kWarps * TOK;
+  static constexpr int WARP = 2 * TOK * RB;        // one stage of one warp: K and V
   static constexpr int STAGE = kWarps * WARP;
   // about 96 KB a CTA, so that two share an SM and ~128 KB an SM are in
   // flight; 256-value rows of 16 bits take 3 stages and the SM alone
@@ -155,6 +173,7 @@ struct AttendArgs {
   const int32_t* page_table;
   const int32_t* seq_lens;
   int max_pages, window, q_bf16;
+  uint32_t div_mul, div_shift;  // position -> page column
   float scale, softcap;
   unsigned* counters;
   float* parts;
@@ -164,8 +183,11 @@ struct AttendArgs {
 // tiles of sequence b: its window is [start, start + n)
 struct Span {
   int start, n;
-  __device__ __forceinline__ int tiles() const { return (n + kTile - 1) / kTile; }
 };
+__device__ __forceinline__ int page_column(const AttendArgs& a, int pos) {
+  // floor(pos / page_size) for pos < 2^31 (multiplier from the host)
+  return (int)(((uint64_t)(uint32_t)pos * a.div_mul) >> a.div_shift);
+}
 __device__ __forceinline__ Span span_of(const AttendArgs& a, int b) {
   const int len0 = a.seq_lens[b];
   const int64_t cap64 = (int64_t)a.max_pages * a.c.page_size;
@@ -179,6 +201,7 @@ __device__ __forceinline__ Span span_of(const AttendArgs& a, int b) {
 }
 
 // walks tiles in (sequence, head block, tile) order
+template <int TILE>
 struct Cursor {
   int b, h, tile, nt;
   Span s;
@@ -190,7 +213,7 @@ struct Cursor {
     do {
       if (++b >= a.B) return;
       s = span_of(a, b);
-      nt = s.tiles();
+      nt = (s.n + TILE - 1) / TILE;
     } while (nt == 0);
   }
 };
@@ -208,10 +231,12 @@ __global__ void __launch_bounds__(kWarps * 32) k_attend(AttendArgs a) {
   using R = Ring<KV, DP>;
   constexpr int MT = KV == MOE_DT_BF16 ? MOE_DT_BF16 : MOE_DT_F16;  // operands' type
   constexpr int RB = R::RB, CPR = RB / 16, S = R::S, KS = DP / 16, NT = DP / 8;
+  constexpr int TOK = R::TOK, TILE = R::TILE, TT = TOK / 8;  // TT: score tiles of 8 tokens
   constexpr int ROWS = 8 * RH, PART = ROWS * (DP + 2);
   extern __shared__ __align__(128) uint8_t ring[];
   float* mb = (float*)(ring + R::BYTES);  // merge buffer: RH 1: two slices of 8 rows, 2: one of 16
   __shared__ float2 ml[kWarps][ROWS];
+  __shared__ float2 joined[kWarps * 32];
   __shared__ uint32_t valid[kWarps][S];
   __shared__ int is_last;
 
@@ -220,35 +245,45 @@ __global__ void __launch_bounds__(kWarps * 32) k_attend(AttendArgs a) {
   pdl_wait();
   pdl_launch_dependents();
 
-  // rows without tokens
-  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-    if (span_of(a, b).n > 0) continue;
-    const int per = a.c.D / 8;
-    for (int i = threadIdx.x; i < a.Hq * per; i += blockDim.x)
-      *(uint4*)((uint16_t*)a.out + b * a.out_row + (i / per) * a.out_head + (i % per) * 8) =
-          make_uint4(0, 0, 0, 0);
-    if (a.lse)
-      for (int i = threadIdx.x; i < a.Hq; i += blockDim.x)
-        a.lse[(int64_t)b * a.Hq + i] = __int_as_float(0xff800000);
-  }
+  // rows without tokens: zeros, while this CTA's first loads are under way
+  auto zero_rows = [&]() {
+    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+      if (span_of(a, b).n > 0) continue;
+      const int per = a.c.D / 8;
+      for (int i = threadIdx.x; i < a.Hq * per; i += blockDim.x)
+        *(uint4*)((uint16_t*)a.out + b * a.out_row + (i / per) * a.out_head + (i % per) * 8) =
+            make_uint4(0, 0, 0, 0);
+      if (a.lse)
+        for (int i = threadIdx.x; i < a.Hq; i += blockDim.x)
+          a.lse[(int64_t)b * a.Hq + i] = __int_as_float(0xff800000);
+    }
+  };
 
   // this CTA's run [u0, u1) of the U tiles
-  long long U = 0;
-  for (int b = lane; b < a.B; b += 32) U += span_of(a, b).tiles();
+  auto tiles_of = [](const Span& s) { return (s.n + TILE - 1) / TILE; };
+  Span s0 = {0, 0};
+  if (lane < a.B) s0 = span_of(a, lane);
+  long long U = tiles_of(s0);
+  for (int b = lane + 32; b < a.B; b += 32) U += tiles_of(span_of(a, b));
 #pragma unroll
   for (int o = 16; o; o >>= 1) U += __shfl_xor_sync(~0u, U, o);
   U *= nh;
   const long long ctas = U < gridDim.x ? U : gridDim.x;
-  if (blockIdx.x >= ctas) return;
+  if (blockIdx.x >= ctas) {
+    zero_rows();
+    return;
+  }
   const long long u0 = blockIdx.x * U / ctas, u1 = (blockIdx.x + 1) * U / ctas;
-  Cursor ci;
+  Cursor<TILE> ci = {};
   {
     long long rem = u0;
-    int b = 0;
     for (int base = 0; base < a.B; base += 32) {
-      Span s = {0, 0};
-      if (base + lane < a.B) s = span_of(a, base + lane);
-      const long long mine = (long long)s.tiles() * nh;
+      Span s = s0;
+      if (base) {
+        s = {0, 0};
+        if (base + lane < a.B) s = span_of(a, base + lane);
+      }
+      const long long mine = (long long)tiles_of(s) * nh;
       long long incl = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -259,49 +294,50 @@ __global__ void __launch_bounds__(kWarps * 32) k_attend(AttendArgs a) {
       if (over) {
         const int src = __ffs(over) - 1;
         rem -= __shfl_sync(~0u, incl - mine, src);
-        b = base + src;
+        ci.b = base + src;
+        ci.s.start = __shfl_sync(~0u, s.start, src);
+        ci.s.n = __shfl_sync(~0u, s.n, src);
+        ci.nt = tiles_of(ci.s);
+        ci.h = (int)(rem / ci.nt);
+        ci.tile = (int)(rem % ci.nt);
         break;
       }
       rem -= __shfl_sync(~0u, incl, 31);
     }
-    ci.b = b;
-    ci.s = span_of(a, b);
-    ci.nt = ci.s.tiles();
-    ci.h = (int)(rem / ci.nt);
-    ci.tile = (int)(rem % ci.nt);
   }
-  Cursor cc = ci;  // ci issues loads ahead of cc, which computes
+  Cursor<TILE> cc = ci;  // ci issues loads ahead of cc, which computes
 
   const uint32_t base = ptx::smem_u32(ring) + w * R::WARP;
   const int nch = a.c.D * R::ES / 16;
   // the page of this lane's token of the tile that is issued next
-  auto page_of = [&](const Cursor& k) {
-    const int rel = k.tile * kTile + w * kTok + (lane & 15);
-    if (k.b >= a.B || rel >= k.s.n) return -1;
-    return a.page_table[(int64_t)k.b * a.table_ld + (k.s.start + rel) / a.c.page_size];
+  auto page_of = [&](const Cursor<TILE>& k) {
+    const int rel = k.tile * TILE + w * TOK + (lane & (TOK - 1));
+    if (rel >= k.s.n) return -1;
+    return a.page_table[(int64_t)k.b * a.table_ld + page_column(a, k.s.start + rel)];
   };
   int page = page_of(ci);
   long long ui = u0;
   auto issue = [&](int stage) {
     if (ui < u1) {
-      const int rel = ci.tile * kTile + w * kTok + (lane & 15);
+      const int rel = ci.tile * TILE + w * TOK + (lane & (TOK - 1));
       const int pos = ci.s.start + rel;
       bool ok = rel < ci.s.n;
       if (ok && (page < 0 || page >= a.c.n_pages)) {
         set_status(a.status, MOE_ERR_DEVICE);
         ok = false;
       }
-      const int64_t off = ok ? (int64_t)page * a.c.page_stride +
-                                   (int64_t)(ci.h / a.nhb) * a.c.head_stride +
-                                   (int64_t)(pos % a.c.page_size) * a.c.token_stride
+      const int at = pos - page_column(a, pos) * a.c.page_size;
+      const int64_t off = ok ? ((int64_t)page * a.c.page_stride +
+                                (int64_t)(ci.h / a.nhb) * a.c.head_stride +
+                                (int64_t)at * a.c.token_stride) * R::ES
                              : 0;
-      const uint32_t mask = __ballot_sync(~0u, ok) & 0xffff;
+      const uint32_t mask = __ballot_sync(~0u, ok) & (TOK == 32 ? ~0u : 0xffffu);
       if (lane == 0) valid[w][stage] = mask;
-      const uint32_t kd = base + stage * R::STAGE, vd = kd + kTok * RB;
+      const uint32_t kd = base + stage * R::STAGE, vd = kd + TOK * RB;
 #pragma unroll
-      for (int i = 0; i < CPR / 2; ++i) {
+      for (int i = 0; i < TOK * CPR / 32; ++i) {
         const int idx = i * 32 + lane, row = idx / CPR, ch = idx % CPR;
-        const int64_t o = __shfl_sync(~0u, off, row) * R::ES + ch * 16;
+        const int64_t o = __shfl_sync(~0u, off, row) + ch * 16;
         const bool v = ((mask >> row) & 1) && ch < nch;
         const uint32_t d = swz<RB>(row, ch);
         cp_async16(kd + d, (const uint8_t*)a.c.k_pages + (v ? o : 0), v ? 16 : 0);
@@ -315,8 +351,6 @@ __global__ void __launch_bounds__(kWarps * 32) k_attend(AttendArgs a) {
     }
     cp_async_commit();
   };
-#pragma unroll
-  for (int i = 0; i < S - 1; ++i) issue(i);
 
   uint32_t qa[KS][2 * RH];
   float acc[NT][4], m[RH], l[RH], sc[RH];
@@ -469,13 +503,25 @@ __global__ void __launch_bounds__(kWarps * 32) k_attend(AttendArgs a) {
       write = is_last;
       if (write) {
         __threadfence();
+        // (M, L) of each row over the parts: a share of them a thread, then over the threads
+        constexpr int Q = kWarps * 32 / ROWS;
+        M = __int_as_float(0xff800000), L = 0.f;
+#pragma unroll 4
+        for (int p = threadIdx.x / ROWS; p < np; p += Q) {
+          const float2 v = __ldcg((const float2*)(part(p) + ROWS * DP) + threadIdx.x % ROWS);
+          const float top = fmaxf(M, v.x);
+          L = L * exp2_approx(M - zero_if_empty(top)) + v.y * exp2_approx(v.x - zero_if_empty(top));
+          M = top;
+        }
+        joined[threadIdx.x] = make_float2(M, L);
+        __syncthreads();
         if (threadIdx.x < ROWS) {
-          M = __int_as_float(0xff800000);
-          for (int p = 0; p < np; ++p)
-            M = fmaxf(M, __ldcg((const float2*)(part(p) + ROWS * DP) + threadIdx.x).x);
+#pragma unroll
+          for (int k = 1; k < Q; ++k) M = fmaxf(M, joined[k * ROWS + threadIdx.x].x);
           L = 0.f;
-          for (int p = 0; p < np; ++p) {
-            const float2 v = __ldcg((const float2*)(part(p) + ROWS * DP) + threadIdx.x);
+#pragma unroll
+          for (int k = 0; k < Q; ++k) {
+            const float2 v = joined[k * ROWS + threadIdx.x];
             L += v.y * exp2_approx(v.x - zero_if_empty(M));
           }
           ml[0][threadIdx.x] = make_float2(M, L);
@@ -485,7 +531,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_attend(AttendArgs a) {
           const int row = (i & 7) + 8 * ((i / 16) % RH);
           const float Mr = zero_if_empty(ml[0][row].x);
           float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 8
           for (int p = 0; p < np; ++p) {
             const float* from = part(p);
             const float4 y = __ldcg((const float4*)from + i);
@@ -537,6 +583,9 @@ __global__ void __launch_bounds__(kWarps * 32) k_attend(AttendArgs a) {
   };
 
   begin_item();
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) issue(i);
+  zero_rows();
   int t0 = cc.tile;
   int stage = 0;
   for (long long u = u0; u < u1; ++u) {
@@ -546,56 +595,73 @@ __global__ void __launch_bounds__(kWarps * 32) k_attend(AttendArgs a) {
       const int to = stage == 0 ? S - 1 : stage - 1;
       issue(to);
     }
-    const uint32_t kd = base + stage * R::STAGE, vd = kd + kTok * RB;
+    const uint32_t kd = base + stage * R::STAGE, vd = kd + TOK * RB;
     const uint32_t mask = valid[w][stage];
 
-    float s[2][4] = {};
-    if constexpr (KV == MOE_DT_E4M3) {
-      const int row = (lane & 7) + ((lane >> 3) & 1) * 8;
+    float s[TT][4] = {};
 #pragma unroll
-      for (int k = 0; k < KS; k += 2) {
-        uint32_t r[4];
-        ldmatrix_x4(r, kd + swz<RB>(row, k + (lane >> 4)));
+    for (int t = 0; t < TOK / 16; ++t) {  // 16 tokens at a time
+      if constexpr (KV == MOE_DT_E4M3) {
+        const int row = t * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int kk = k + (i >> 1);
-          uint32_t qf[4];
-          qf[0] = qa[kk][0], qf[1] = RH == 2 ? qa[kk][RH - 1] : 0u;
-          qf[2] = qa[kk][RH], qf[3] = RH == 2 ? qa[kk][2 * RH - 1] : 0u;
-          mma16816<MT>(s[i & 1], qf, e4m3x2_to_f16x2(r[i] & 0xffff), e4m3x2_to_f16x2(r[i] >> 16));
+        for (int k = 0; k < KS; k += 2) {
+          uint32_t r[4];
+          ldmatrix_x4(r, kd + swz<RB>(row, k + (lane >> 4)));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int kk = k + (i >> 1);
+            const uint32_t qf[4] = {qa[kk][0], RH == 2 ? qa[kk][RH - 1] : 0u, qa[kk][RH],
+                                    RH == 2 ? qa[kk][2 * RH - 1] : 0u};
+            uint32_t b0, b1;
+            e4m3x4_to_f16x2x2(r[i], b0, b1);
+            mma16816<MT>(s[2 * t + (i & 1)], qf, b0, b1);
+          }
         }
-      }
-    } else {
-      const int row = (lane & 7) + (lane >> 4) * 8;
+      } else {
+        const int row = t * 16 + (lane & 7) + (lane >> 4) * 8;
 #pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        uint32_t r[4];
-        ldmatrix_x4(r, kd + swz<RB>(row, 2 * k + ((lane >> 3) & 1)));
-        uint32_t qf[4];
-        qf[0] = qa[k][0], qf[1] = RH == 2 ? qa[k][RH - 1] : 0u;
-        qf[2] = qa[k][RH], qf[3] = RH == 2 ? qa[k][2 * RH - 1] : 0u;
-        mma16816<MT>(s[0], qf, r[0], r[1]);
-        mma16816<MT>(s[1], qf, r[2], r[3]);
+        for (int k = 0; k < KS; ++k) {
+          uint32_t r[4];
+          ldmatrix_x4(r, kd + swz<RB>(row, 2 * k + ((lane >> 3) & 1)));
+          const uint32_t qf[4] = {qa[k][0], RH == 2 ? qa[k][RH - 1] : 0u, qa[k][RH],
+                                  RH == 2 ? qa[k][2 * RH - 1] : 0u};
+          mma16816<MT>(s[2 * t], qf, r[0], r[1]);
+          mma16816<MT>(s[2 * t + 1], qf, r[2], r[3]);
+        }
       }
     }
 
     // scores in units of log2, running maximum and sum
-    float p[2][2 * RH];
     bool grew = false;
     float al[RH];
 #pragma unroll
     for (int r = 0; r < RH; ++r) {
+      if (a.softcap > 0.f) {
+        // cap * tanh(v / cap) = cap * (1 - 2 / (e^(2 v / cap) + 1)): its error is
+        // a few 2^-24 of the cap, as absolute as the softmax takes it
+        const float in = sc[r] * (2.f * kLog2e / a.softcap), cap = a.softcap * kLog2e;
+#pragma unroll
+        for (int i = 0; i < TT; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            s[i][2 * r + j] = cap - 2.f * cap * rcp_approx(exp2_approx(s[i][2 * r + j] * in) + 1.f);
+      } else {
+        const float k = sc[r] * kLog2e;
+#pragma unroll
+        for (int i = 0; i < TT; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) s[i][2 * r + j] *= k;
+      }
+      if (mask != (TOK == 32 ? ~0u : 0xffffu)) {
+#pragma unroll
+        for (int i = 0; i < TT; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            if (!((mask >> (i * 8 + c4 * 2 + j)) & 1)) s[i][2 * r + j] = __int_as_float(0xff800000);
+      }
       float top = m[r];
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float v = s[i][2 * r + j] * sc[r];
-          if (a.softcap > 0.f) v = a.softcap * tanhf(v / a.softcap);
-          v = (mask >> (i * 8 + c4 * 2 + j)) & 1 ? v * kLog2e : __int_as_float(0xff800000);
-          p[i][2 * r + j] = v;
-          top = fmaxf(top, v);
-        }
+      for (int i = 0; i < TT; ++i) top = fmaxf(top, fmaxf(s[i][2 * r], s[i][2 * r + 1]));
       top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
       top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
       const float z = top == __int_as_float(0xff800000) ? 0.f : top;
@@ -604,11 +670,11 @@ __global__ void __launch_bounds__(kWarps * 32) k_attend(AttendArgs a) {
       m[r] = top;
       float sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < TT; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          p[i][2 * r + j] = exp2_approx(p[i][2 * r + j] - z);
-          sum += p[i][2 * r + j];
+          s[i][2 * r + j] = exp2_approx(s[i][2 * r + j] - z);
+          sum += s[i][2 * r + j];
         }
       l[r] = l[r] * al[r] + sum;
     }
@@ -618,50 +684,53 @@ __global__ void __launch_bounds__(kWarps * 32) k_attend(AttendArgs a) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] *= al[RH == 1 ? 0 : j >> 1];
     }
-    // P as the sum of two 16-bit numbers (hi + lo, 16 or 22 bits): rounding it
-    // once to bf16 would cost as much as the output's own rounding.  With up
-    // to 8 heads the lo parts ride in the tile's other 8 rows, at no cost.
-    uint32_t hi[4], lo[4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int t = 0; t < TOK / 16; ++t) {
+      // P as the sum of two 16-bit numbers (hi + lo, 16 or 22 bits): rounding it
+      // once to bf16 would cost as much as the output's own rounding.  With up
+      // to 8 heads the lo parts ride in the tile's other 8 rows, at no cost.
+      uint32_t hi[4], lo[4];
 #pragma unroll
-      for (int r = 0; r < RH; ++r) {
-        const float x = p[i][2 * r], y = p[i][2 * r + 1];
-        const uint32_t h = pack2<MT>(x, y);
-        const uint32_t rest = pack2<MT>(x - lo2<MT>(h), y - hi2<MT>(h));
-        if constexpr (RH == 1) {
-          hi[2 * i] = h;
-          hi[2 * i + 1] = rest;
-        } else {
-          hi[2 * i + r] = h;
-          lo[2 * i + r] = rest;
-        }
-      }
-    const int row = (lane & 7) + ((lane >> 3) & 1) * 8;
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int k = 0; k < CPR; k += 2) {
-      uint32_t r[4];
-      ldmatrix_x4_trans(r, vd + swz<RB>(row, k + (lane >> 4)));
-      if constexpr (KV == MOE_DT_E4M3) {
-        // a 16-bit element holds values 2n, 2n + 1 of a token; a register two
-        // tokens' pairs.  Bytes 0, 2 (values 2n) feed one tile, 1, 3 the next.
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t x = __byte_perm(r[2 * i], 0, 0x3120), y = __byte_perm(r[2 * i + 1], 0, 0x3120);
-#pragma unroll
-          for (int o = 0; o < 2; ++o) {
-            const uint32_t b0 = e4m3x2_to_f16x2(o ? x >> 16 : x & 0xffff);
-            const uint32_t b1 = e4m3x2_to_f16x2(o ? y >> 16 : y & 0xffff);
-            mma16816<MT>(acc[2 * (k + i) + o], hi, b0, b1);
-            if constexpr (RH == 2) mma16816<MT>(acc[2 * (k + i) + o], lo, b0, b1);
+        for (int r = 0; r < RH; ++r) {
+          const float x = s[2 * t + i][2 * r], y = s[2 * t + i][2 * r + 1];
+          const uint32_t h = pack2<MT>(x, y);
+          const uint32_t rest = pack2<MT>(x - lo2<MT>(h), y - hi2<MT>(h));
+          if constexpr (RH == 1) {
+            hi[2 * i] = h;
+            hi[2 * i + 1] = rest;
+          } else {
+            hi[2 * i + r] = h;
+            lo[2 * i + r] = rest;
           }
         }
-      } else {
-        mma16816<MT>(acc[k], hi, r[0], r[1]);
-        mma16816<MT>(acc[k + 1], hi, r[2], r[3]);
-        if constexpr (RH == 2) {
-          mma16816<MT>(acc[k], lo, r[0], r[1]);
-          mma16816<MT>(acc[k + 1], lo, r[2], r[3]);
+      const int row = t * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
+#pragma unroll
+      for (int k = 0; k < CPR; k += 2) {
+        uint32_t r[4];
+        ldmatrix_x4_trans(r, vd + swz<RB>(row, k + (lane >> 4)));
+        if constexpr (KV == MOE_DT_E4M3) {
+          // a 16-bit element holds values 2n, 2n + 1 of a token; a register two
+          // tokens' pairs.  Bytes 0, 2 (values 2n) feed one tile, 1, 3 the next.
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint32_t x[2], y[2];
+            e4m3x4_to_f16x2x2(__byte_perm(r[2 * i], 0, 0x3120), x[0], x[1]);
+            e4m3x4_to_f16x2x2(__byte_perm(r[2 * i + 1], 0, 0x3120), y[0], y[1]);
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {
+              mma16816<MT>(acc[2 * (k + i) + o], hi, x[o], y[o]);
+              if constexpr (RH == 2) mma16816<MT>(acc[2 * (k + i) + o], lo, x[o], y[o]);
+            }
+          }
+        } else {
+          mma16816<MT>(acc[k], hi, r[0], r[1]);
+          mma16816<MT>(acc[k + 1], hi, r[2], r[3]);
+          if constexpr (RH == 2) {
+            mma16816<MT>(acc[k], lo, r[0], r[1]);
+            mma16816<MT>(acc[k + 1], lo, r[2], r[3]);
+          }
         }
       }
     }
@@ -696,7 +765,8 @@ moe_status launch_attend(const AttendArgs& a, cudaStream_t s) {
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
   // no more CTAs than tiles there can be
-  const int64_t tiles = ((int64_t)a.max_pages * a.c.page_size + kTile - 1) / kTile;
+  constexpr int TILE = Ring<KV, DP>::TILE;
+  const int64_t tiles = ((int64_t)a.max_pages * a.c.page_size + TILE - 1) / TILE;
   const double most = (double)a.B * a.c.Hkv * a.nhb * (double)(tiles > 0 ? tiles : 1);
   const int resident = smem > 113 * 1024 ? kSMs : kMaxCtas;
   const int grid = most < resident ? (int)most : resident;
@@ -806,6 +876,10 @@ MOE_API moe_status kvcache_attend(const kvcache_attend_args* a, void* stream) {
   k.table_ld = a->table_ld, k.page_table = a->page_table, k.seq_lens = a->seq_lens;
   k.max_pages = a->max_pages, k.window = a->window, k.q_bf16 = a->dtype == MOE_DT_BF16;
   k.scale = a->scale, k.softcap = a->softcap;
+  // for pos < 2^31: floor(pos / d) = pos * ceil(2^(31 + s) / d) >> (31 + s), 2^s >= d
+  k.div_shift = 31;
+  while ((1ull << (k.div_shift - 31)) < (uint64_t)a->c.page_size) ++k.div_shift;
+  k.div_mul = (uint32_t)(((1ull << k.div_shift) + a->c.page_size - 1) / a->c.page_size);
   k.counters = (unsigned*)a->workspace;
   k.parts = (float*)((uint8_t*)a->workspace + kCtlBytes);
   k.status = a->status;
