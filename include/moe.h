@@ -684,9 +684,8 @@ moe_status kvcache_attend(const kvcache_attend_args* a, void* stream);
  * [N][ceil(K/group / 2)].  scales [N][K/group], bias and x, y of `dtype`.
  * Products are exact and sums fp32.  Meant for few tokens: the weights are
  * read once for every 16 of them.
- * K a multiple of group, group a multiple of 32, K / group <= 1024; codes and
- * x 16-byte aligned, ldx a multiple of 8; else MOE_ERR_UNSUPPORTED.  T == 0 is
- * a no-op. */
+ * K a multiple of group, group a multiple of 32; codes and x 16-byte aligned,
+ * ldx a multiple of 8; else MOE_ERR_UNSUPPORTED.  T == 0 is a no-op. */
 enum { MOE_W4_U4 = 0, MOE_W4_E2M1 = 1 };
 
 typedef struct {

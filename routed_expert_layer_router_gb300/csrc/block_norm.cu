@@ -178,135 +178,281 @@ __global__ void __launch_bounds__(MAXT) k_block_norm(NormArgs a) {
   }
 }
 
-// Many rows: a CTA stays and walks rows t, t + grid, ...  A thread owns 8 values
-// of every row, so the weights (and a channel gate) stay in its registers, and
-// its share of the next rows' x, y (and gate) comes ahead into shared memory by
+// packed pairs of fp32: one instruction for two values
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " mov.b64 c, {%6, %7};\n fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " mul.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " add.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+// sums of two rows at once over the CTA: after the first exchange a lane carries
+// one row only, so two sums cost the shuffles of little more than one
+__device__ __forceinline__ float2 block_sum2(float2 v, float (*part)[64], int& slot) {
+  const int lane = threadIdx.x & 31, up = lane >> 4, warps = blockDim.x >> 5;
+  float mine = up ? v.y : v.x;
+  mine += __shfl_xor_sync(~0u, up ? v.x : v.y, 16);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) mine += __shfl_xor_sync(~0u, mine, o);
+  if (warps > 1) {
+    if ((lane & 15) == 0) part[slot][up * 32 + (threadIdx.x >> 5)] = mine;
+    __syncthreads();
+    const float* p = part[slot] + up * 32;
+    const int k = lane & 15;
+    mine = (k < warps ? p[k] : 0.f) + (k + 16 < warps ? p[k + 16] : 0.f);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) mine += __shfl_xor_sync(~0u, mine, o);
+    slot ^= 1;
+  }
+  const float other = __shfl_xor_sync(~0u, mine, 16);
+  return up ? make_float2(other, mine) : make_float2(mine, other);
+}
+
+// Many rows: a CTA stays and walks pairs of rows.  A thread owns 8 values of
+// every row, so the weights (and a channel gate) stay in its registers, and its
+// share of the next pairs' x, y (and gate) comes ahead into shared memory by
 // cp.async: a thread reads back only what it copied itself, so the ring needs
-// no barrier, and memory stays busy while a row's two reductions run.
+// no barrier, and memory stays busy while the pair's two reductions run.  Two
+// rows at a time halve the barriers, and packed fp32 the arithmetic.
+// The 8 values are 8 in a row where all are 16 bits wide, else 4 and 4 (half a
+// row apart), so that a warp's fp32 accesses are whole runs of 512 bytes.
 template <int RT, int BT, int MAXT>
 __global__ void __launch_bounds__(MAXT) k_block_norm_rows(NormArgs a, int stages) {
-  constexpr int XV = RT == MOE_DT_F32 ? 2 : 1, BV = BT == MOE_DT_F32 ? 2 : 1;  // 16-byte pieces
-  extern __shared__ __align__(16) uint4 ring[];
-  __shared__ float part[2][32];
+  constexpr bool SPLIT = RT == MOE_DT_F32;
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ float part[2][64];
   int slot = 0;
-  const int i = threadIdx.x * 8, nthr = blockDim.x;
-  const bool in = i < a.H;
+  const int tid = threadIdx.x, nthr = blockDim.x;
+  const int o0 = SPLIT ? tid * 4 : tid * 8, o1 = SPLIT ? (tid + nthr) * 4 : tid * 8 + 4;
+  const bool in0 = o0 < a.H, in1 = o1 < a.H;
   const bool full_gate = a.gate && a.gate_col && a.gate_row;
-  const int planes = XV + (a.y ? BV : 0) + (full_gate ? BV : 0);
+  constexpr int XB = RT == MOE_DT_F32 ? 32 : 16, BB = BT == MOE_DT_F32 ? 32 : 16;  // of a thread
+  const int row_bytes = (XB + (a.y ? BB : 0) + (full_gate ? BB : 0)) * nthr;
   const float inv_h = 1.f / (float)a.H;
   pdl_wait();
   pdl_launch_dependents();
 
-  const uint32_t mine = (uint32_t)__cvta_generic_to_shared(ring) + threadIdx.x * 16;
-  auto issue = [&](int64_t t, int stage) {
-    if (t < a.T && in) {
-      uint32_t d = mine + stage * planes * nthr * 16;
-      auto copy = [&](const void* p, int n) {
-        for (int k = 0; k < n; ++k, d += nthr * 16) cp_async16(d, (const uint8_t*)p + k * 16, 16);
-      };
-      copy((const typename Elem<RT>::T*)a.x + t * a.ldx + i, XV);
-      if (a.y) copy((const typename Elem<BT>::T*)a.y + t * a.ldy + i, BV);
-      if (full_gate) copy((const typename Elem<BT>::T*)a.gate + t * a.gate_row + i, BV);
+  // a row's share of this thread, as it lies in the ring
+  auto copy = [&](auto dt, const void* p, uint32_t d) {
+    constexpr int DT = decltype(dt)::value;
+    const typename Elem<DT>::T* q = (const typename Elem<DT>::T*)p;
+    if constexpr (DT == MOE_DT_F32) {
+      if (in0) cp_async16(d + tid * 16, q + o0, 16);
+      if (in1) cp_async16(d + (tid + nthr) * 16, q + o1, 16);
+    } else if constexpr (SPLIT) {
+      if (in0) cp_async8(d + tid * 8, q + o0);
+      if (in1) cp_async8(d + (tid + nthr) * 8, q + o1);
+    } else {
+      if (in0) cp_async16(d + tid * 16, q + o0, 16);
+    }
+  };
+  auto unpack4 = [](auto dt, const uint2& u, float2* v) {
+    constexpr int DT = decltype(dt)::value;
+    v[0] = make_float2(lo2<DT>(u.x), hi2<DT>(u.x));
+    v[1] = make_float2(lo2<DT>(u.y), hi2<DT>(u.y));
+  };
+  auto take = [&](auto dt, const uint8_t* d, float2 (&v)[4]) {
+    constexpr int DT = decltype(dt)::value;
+    if constexpr (DT == MOE_DT_F32) {
+      const float4 x = *(const float4*)(d + tid * 16), y = *(const float4*)(d + (tid + nthr) * 16);
+      v[0] = make_float2(x.x, x.y), v[1] = make_float2(x.z, x.w);
+      v[2] = make_float2(y.x, y.y), v[3] = make_float2(y.z, y.w);
+    } else if constexpr (SPLIT) {
+      unpack4(dt, *(const uint2*)(d + tid * 8), v);
+      unpack4(dt, *(const uint2*)(d + (tid + nthr) * 8), v + 2);
+    } else {
+      const uint4 u = *(const uint4*)(d + tid * 16);
+      unpack4(dt, make_uint2(u.x, u.y), v);
+      unpack4(dt, make_uint2(u.z, u.w), v + 2);
+    }
+  };
+  // straight from and to global memory, at o0 and o1
+  auto load_at = [&](auto dt, const void* p, float2 (&v)[4]) {
+    constexpr int DT = decltype(dt)::value;
+    const typename Elem<DT>::T* q = (const typename Elem<DT>::T*)p;
+    if constexpr (DT == MOE_DT_F32) {
+      const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+      const float4 x = in0 ? *(const float4*)(q + o0) : z, y = in1 ? *(const float4*)(q + o1) : z;
+      v[0] = make_float2(x.x, x.y), v[1] = make_float2(x.z, x.w);
+      v[2] = make_float2(y.x, y.y), v[3] = make_float2(y.z, y.w);
+    } else {
+      const uint2 z = make_uint2(0, 0);
+      unpack4(dt, in0 ? *(const uint2*)(q + o0) : z, v);
+      unpack4(dt, in1 ? *(const uint2*)(q + o1) : z, v + 2);
+    }
+  };
+  auto put = [&](auto dt, void* p, const float2 (&v)[4]) {
+    constexpr int DT = decltype(dt)::value;
+    typename Elem<DT>::T* q = (typename Elem<DT>::T*)p;
+    if constexpr (DT == MOE_DT_F32) {
+      if (in0) *(float4*)(q + o0) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+      if (in1) *(float4*)(q + o1) = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+    } else {
+      const uint2 x = make_uint2(pack2<DT>(v[0].x, v[0].y), pack2<DT>(v[1].x, v[1].y));
+      const uint2 y = make_uint2(pack2<DT>(v[2].x, v[2].y), pack2<DT>(v[3].x, v[3].y));
+      if constexpr (SPLIT) {
+        if (in0) *(uint2*)(q + o0) = x;
+        if (in1) *(uint2*)(q + o1) = y;
+      } else if (in0) {
+        *(uint4*)(q + o0) = make_uint4(x.x, x.y, y.x, y.y);
+      }
+    }
+  };
+  const std::integral_constant<int, RT> rt;
+  const std::integral_constant<int, BT> bt;
+  const std::integral_constant<int, MOE_DT_F32> f32;
+  using RE = typename Elem<RT>::T;
+  using BE = typename Elem<BT>::T;
+
+  const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
+  const int64_t pairs = ((int64_t)a.T + 1) / 2;
+  auto issue = [&](int64_t pair, int stage) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int64_t t = 2 * pair + q;
+      if (t < a.T) {
+        uint32_t d = ring_at + (stage * 2 + q) * row_bytes;
+        copy(rt, (const RE*)a.x + t * a.ldx, d);
+        if (a.y) copy(bt, (const BE*)a.y + t * a.ldy, d + XB * nthr);
+        if (full_gate) copy(bt, (const BE*)a.gate + t * a.gate_row, d + (XB + BB) * nthr);
+      }
     }
     cp_async_commit();
   };
   const int64_t step = gridDim.x;
   for (int k = 0; k < stages - 1; ++k) issue(blockIdx.x + k * step, k);
 
-  float w_post[8], w_pre[8], cg[8];
-  auto weights = [&](const void* w, float (&v)[8], float off) {
+  float2 w_post[4], w_pre[4], cg[4];
+  auto vector = [&](const void* w, float2 (&v)[4]) {
+    if (a.w16) load_at(bt, w, v);
+    else load_at(f32, w, v);
+  };
+  auto weights = [&](const void* w, float2 (&v)[4]) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = 1.f;
-    if (w && in) {
-      if (a.w16) load<BT, 8>(w, i, v);
-      else load<MOE_DT_F32, 8>(w, i, v);
+    for (int j = 0; j < 4; ++j) v[j] = make_float2(1.f, 1.f);
+    if (w) {
+      vector(w, v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] += off;
+      for (int j = 0; j < 4; ++j) v[j] = add2(v[j], make_float2(a.w_offset, a.w_offset));
     }
   };
   auto gated = [&](float v) {
     return a.branch_scale * (a.gate_act == MOE_GATE_SIGMOID ? 1.f / (1.f + expf(-v)) : v);
   };
-  weights(a.w_post, w_post, a.w_offset);
-  weights(a.w_pre, w_pre, a.w_offset);
+  weights(a.w_post, w_post);
+  weights(a.w_pre, w_pre);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) cg[j] = a.branch_scale;
-  if (a.gate && a.gate_col && !a.gate_row && in) {
-    load<BT, 8>(a.gate, i, cg);
+  for (int j = 0; j < 4; ++j) cg[j] = make_float2(a.branch_scale, a.branch_scale);
+  if (a.gate && a.gate_col && !a.gate_row) {
+    load_at(bt, a.gate, cg);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) cg[j] = gated(cg[j]);
+    for (int j = 0; j < 4; ++j) cg[j] = make_float2(gated(cg[j].x), gated(cg[j].y));
   }
 
-  auto norm = [&](float (&v)[8], const float (&w)[8], const void* c) {
-    float mean = 0.f;
+  // sum of this thread's terms of a row; what lies outside it counts nothing
+  auto own = [&](const float2& u, const float2& v) {
+    return (in0 ? u.x + u.y : 0.f) + (in1 ? v.x + v.y : 0.f);
+  };
+  auto norm = [&](float2 (&v)[2][4], const float2 (&w)[4], const void* c) {
     if (a.kind == MOE_NORM_LAYER) {
-      float s = 0.f;
+      float s[2];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s += v[j];
-      mean = block_sum(in ? s : 0.f, part, slot) * inv_h;
+      for (int q = 0; q < 2; ++q) s[q] = own(add2(v[q][0], v[q][1]), add2(v[q][2], v[q][3]));
+      const float2 mean = block_sum2(make_float2(s[0], s[1]), part, slot);
+      const float m[2] = {-mean.x * inv_h, -mean.y * inv_h};
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[q][j] = add2(v[q][j], make_float2(m[q], m[q]));
     }
-    float s = 0.f;
+    float s[2];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      v[j] -= mean;
-      s += v[j] * v[j];
-    }
-    const float rs = rsqrtf(block_sum(in ? s : 0.f, part, slot) * inv_h + a.eps);
+    for (int q = 0; q < 2; ++q)
+      s[q] = own(fma2(v[q][1], v[q][1], mul2(v[q][0], v[q][0])),
+                 fma2(v[q][3], v[q][3], mul2(v[q][2], v[q][2])));
+    const float2 sq = block_sum2(make_float2(s[0], s[1]), part, slot);
+    const float rs[2] = {rsqrtf(sq.x * inv_h + a.eps), rsqrtf(sq.y * inv_h + a.eps)};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] *= rs * w[j];
-    if (c && in) {
-      float u[8];
-      if (a.w16) load<BT, 8>(c, i, u);
-      else load<MOE_DT_F32, 8>(c, i, u);
+    for (int q = 0; q < 2; ++q)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] += u[j];
+      for (int j = 0; j < 4; ++j) v[q][j] = mul2(mul2(v[q][j], make_float2(rs[q], rs[q])), w[j]);
+    if (c) {
+      float2 u[4];
+      vector(c, u);
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[q][j] = add2(v[q][j], u[j]);
     }
   };
 
   int stage = 0;
-  for (int64_t t = blockIdx.x; t < a.T; t += step) {
-    // the oldest group is this row's; an empty group keeps the count at the end
+  for (int64_t pair = blockIdx.x; pair < pairs; pair += step) {
+    // the oldest group is this pair's; an empty group keeps the count at the end
     if (stages == 2) cp_async_wait<0>();
     else if (stages == 3) cp_async_wait<1>();
-    else if (stages == 4) cp_async_wait<2>();
-    else cp_async_wait<3>();
-    float r[8] = {}, b[8] = {}, g[8];
-    const uint4* p = ring + stage * planes * nthr + threadIdx.x;
-    auto take = [&](auto dt, float (&v)[8]) {
-      constexpr int DT = decltype(dt)::value;
-      uint4 q[2];
-      q[0] = p[0];
-      if constexpr (DT == MOE_DT_F32) q[1] = p[nthr];
-      load8<DT>(q, v);
-      p += (DT == MOE_DT_F32 ? 2 : 1) * nthr;
-    };
-    if (in) {
-      take(std::integral_constant<int, RT>(), r);
-      if (a.y) take(std::integral_constant<int, BT>(), b);
+    else cp_async_wait<2>();
+    const int64_t t = 2 * pair;
+    const bool two = t + 1 < a.T;
+    float2 r[2][4] = {}, b[2][4] = {};
+    const uint8_t* row = ring + stage * 2 * row_bytes;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      if (q == 0 || two) {
+        take(rt, row + q * row_bytes, r[q]);
+        if (a.y) take(bt, row + q * row_bytes + XB * nthr, b[q]);
+      }
     }
-    if (full_gate && in) {
-      take(std::integral_constant<int, BT>(), g);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) g[j] = gated(g[j]);
-    } else if (a.gate && !a.gate_col) {
-      float one[1];
-      load<BT, 1>(a.gate, t * a.gate_row, one);
-      one[0] = gated(one[0]);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) g[j] = one[0];
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) g[j] = cg[j];
-    }
-    issue(t + (stages - 1) * step, stage == 0 ? stages - 1 : stage - 1);
-    stage = stage + 1 == stages ? 0 : stage + 1;
     if (a.post_norm) norm(b, w_post, a.b_post);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) r[j] = a.res_scale * r[j] + g[j] * b[j];
-    if (a.r && in) store<RT, 8>(a.r, t * a.ldr + i, r);
+    for (int q = 0; q < 2; ++q) {
+      if (q == 1 && !two) continue;
+      float2 g[4];
+      if (full_gate) {
+        take(bt, row + q * row_bytes + (XB + BB) * nthr, g);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) g[j] = make_float2(gated(g[j].x), gated(g[j].y));
+      } else if (a.gate && !a.gate_col) {
+        float one[1];
+        load<BT, 1>(a.gate, (t + q) * a.gate_row, one);
+        one[0] = gated(one[0]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) g[j] = make_float2(one[0], one[0]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) g[j] = cg[j];
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        r[q][j] = fma2(r[q][j], make_float2(a.res_scale, a.res_scale), mul2(b[q][j], g[j]));
+      if (a.r) put(rt, (RE*)a.r + (t + q) * a.ldr, r[q]);
+    }
+    // this pair's stage has been read: the pair `stages - 1` ahead goes behind it
+    issue(pair + (stages - 1) * step, stage == 0 ? stages - 1 : stage - 1);
+    stage = stage + 1 == stages ? 0 : stage + 1;
     if (a.h) {
       norm(r, w_pre, a.b_pre);
-      if (in) store<BT, 8>(a.h, t * a.ldh + i, r);
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        if (q == 0 || two) put(bt, (BE*)a.h + (t + q) * a.ldh, r[q]);
     }
   }
   cp_async_wait<0>();
@@ -330,16 +476,17 @@ cudaError_t launch_rows(const NormArgs& a, cudaStream_t s) {
   const int planes = (RT == MOE_DT_F32 ? 2 : 1) +
                      (BT == MOE_DT_F32 ? 2 : 1) *
                          ((a.y ? 1 : 0) + (a.gate && a.gate_col && a.gate_row ? 1 : 0));
-  const int row = planes * threads * 16;
-  // registers allow 64K / (threads * (64 or 80)) rows an SM; the ring gets as
-  // deep as shared memory then allows, 5 at most
+  const int pair = 2 * planes * threads * 16;
+  // registers allow 64K / (threads * (64 or 80)) CTAs an SM; the ring gets as
+  // deep as shared memory then allows, 4 pairs at most
   int per_sm = 65536 / (threads * (MAXT <= 768 ? 80 : 64));
   if (per_sm > 24) per_sm = 24;
-  int stages = kMost / per_sm / row;
-  stages = stages > 5 ? 5 : stages < 2 ? 2 : stages;
-  while (per_sm > 1 && per_sm * (stages * row + 1280) > 227 * 1024) --per_sm;
-  const int grid = a.T < per_sm * kSMs ? a.T : per_sm * kSMs;
-  return launch_pdl(kern, grid, threads, (size_t)stages * row, s, a, stages);
+  int stages = kMost / per_sm / pair;
+  stages = stages > 4 ? 4 : stages < 2 ? 2 : stages;
+  while (per_sm > 1 && per_sm * (stages * pair + 1536) > 227 * 1024) --per_sm;
+  const int pairs = (a.T + 1) / 2;
+  const int grid = pairs < per_sm * kSMs ? pairs : per_sm * kSMs;
+  return launch_pdl(kern, grid, threads, (size_t)stages * pair, s, a, stages);
 }
 
 template <int RT, int BT, int VEC, int VPT, int MAXT>

@@ -18,7 +18,7 @@ namespace {
 constexpr int kAppendThreads = 256;
 
 template <int DT, int KV>
-__global__ void __launch_bounds__(kAppendThreads) k_append(kvcache_append_args a) {
+__global__ void __launch_bounds__(kAppendThreads, 4) k_append(kvcache_append_args a) {
   using E = uint16_t;
   pdl_wait();
   pdl_launch_dependents();
@@ -115,11 +115,20 @@ __global__ void __launch_bounds__(kAppendThreads) k_append(kvcache_append_args a
       store8<DT>(dst + d1, w);
     } else if constexpr (KV == MOE_DT_E4M3) {
       const float* sc = is_k ? a.c.k_scale : a.c.v_scale;
-      const float s = sc ? sc[kh] : 1.f;
+      const float s = sc ? sc[kh] : 1.f, inv = 1.f / s;
+      // x / s rounded as the division rounds it: x * (1 / s) and one correction by
+      // its exact remainder (Markstein 1990); large quotients saturate anyway, and
+      // an infinite one has no remainder
+      auto over = [&](float x) {
+        const float q = x * inv;
+        return fabsf(q) < 1024.f ? fmaf(fmaf(-q, s, x), inv, q) : q;
+      };
       uint8_t* dst = (uint8_t*)(is_k ? a.c.k_pages : a.c.v_pages) + base + kh * a.c.head_stride;
       auto put = [&](uint8_t* p, const float (&x)[8]) {
-        uint32_t lo = pack_e4m3(x[0] / s, x[1] / s) | (uint32_t)pack_e4m3(x[2] / s, x[3] / s) << 16;
-        uint32_t hi = pack_e4m3(x[4] / s, x[5] / s) | (uint32_t)pack_e4m3(x[6] / s, x[7] / s) << 16;
+        uint32_t lo = pack_e4m3(over(x[0]), over(x[1])) |
+                      (uint32_t)pack_e4m3(over(x[2]), over(x[3])) << 16;
+        uint32_t hi = pack_e4m3(over(x[4]), over(x[5])) |
+                      (uint32_t)pack_e4m3(over(x[6]), over(x[7])) << 16;
         *(uint2*)p = make_uint2(lo, hi);
       };
       put(dst + d0, u);
@@ -236,7 +245,6 @@ __global__ void __launch_bounds__(kWarps * 32) k_attend(AttendArgs a) {
   extern __shared__ __align__(128) uint8_t ring[];
   float* mb = (float*)(ring + R::BYTES);  // merge buffer: RH 1: two slices of 8 rows, 2: one of 16
   __shared__ float2 ml[kWarps][ROWS];
-  __shared__ float2 joined[kWarps * 32];
   __shared__ uint32_t valid[kWarps][S];
   __shared__ int is_last;
 
@@ -263,12 +271,23 @@ __global__ void __launch_bounds__(kWarps * 32) k_attend(AttendArgs a) {
   auto tiles_of = [](const Span& s) { return (s.n + TILE - 1) / TILE; };
   Span s0 = {0, 0};
   if (lane < a.B) s0 = span_of(a, lane);
-  long long U = tiles_of(s0);
-  for (int b = lane + 32; b < a.B; b += 32) U += tiles_of(span_of(a, b));
+  int most = tiles_of(s0);
+  long long U = most;
+  for (int b = lane + 32; b < a.B; b += 32) {
+    const int t = tiles_of(span_of(a, b));
+    U += t;
+    most = max(most, t);
+  }
+  const int longest = __reduce_max_sync(~0u, most);
 #pragma unroll
   for (int o = 16; o; o >>= 1) U += __shfl_xor_sync(~0u, U, o);
   U *= nh;
-  const long long ctas = U < gridDim.x ? U : gridDim.x;
+  // A CTA more costs an item's join another part, a tile more costs its CTA the
+  // tile: runs of about sqrt(n / 2) tiles for items of n, unless the GPU is full
+  int run = 1;
+  while (2 * (run + 1) * (run + 1) <= longest) ++run;
+  const long long want = (U + run - 1) / run;
+  const long long ctas = want < gridDim.x ? want : gridDim.x;
   if (blockIdx.x >= ctas) {
     zero_rows();
     return;
@@ -415,37 +434,39 @@ __global__ void __launch_bounds__(kWarps * 32) k_attend(AttendArgs a) {
     }
   };
 
-  // all warps' results of an item: to the output, or a part of it to the
-  // workspace; t0, t1: the tiles of the item that this run covered
-  auto end_item = [&](long long first_u, int t0, int t1) {
-    const int kvh = cc.h / a.nhb, hb = cc.h % a.nhb;
-#pragma unroll
-    for (int r = 0; r < RH; ++r) {
-      l[r] += __shfl_xor_sync(~0u, l[r], 1);
-      l[r] += __shfl_xor_sync(~0u, l[r], 2);
-      if (c4 == 0) ml[w][r * 8 + g] = make_float2(m[r], l[r]);
-    }
-    __syncthreads();
-    auto top_of = [&](int row) {
-      float M = ml[0][row].x;
-#pragma unroll
-      for (int i = 1; i < kWarps; ++i) M = fmaxf(M, ml[i][row].x);
-      return M;
-    };
-    auto zero_if_empty = [](float M) { return M == __int_as_float(0xff800000) ? 0.f : M; };
-    float f[RH];
-#pragma unroll
-    for (int r = 0; r < RH; ++r) f[r] = exp2_approx(m[r] - zero_if_empty(top_of(r * 8 + g)));
-    // value (n tile i, row half r, column j) of this lane
+  // ---- the end of an item
+  auto zero_if_empty = [](float M) { return M == __int_as_float(0xff800000) ? 0.f : M; };
+  // Scaled sums of the warps meet in shared memory, in the fragments' order:
+  // value (n tile i, row half r, column j) of a lane at ((i RH + r) 2 + j) 32 +
+  // lane.  Once the ring has nothing left to bring (`idle`), each warp lays its
+  // sums into its own part of it; otherwise the warps add into the merge buffer
+  // (two slices of 8 rows, one of 16) one after another.
+  constexpr int SLICE = ROWS * DP;
+  auto slice_at = [&](int warp, int off) {  // of the ring: float `off` of a warp's slice
+    const int b = off * 4;
+    return (float*)(ring + (b / R::WARP) * R::STAGE + warp * R::WARP + b % R::WARP);
+  };
+  static_assert(SLICE * 4 <= S * R::WARP, "a warp's sums fit its ring");
+  auto lay = [&](bool idle, const float (&f)[RH]) {
     auto value = [&](int i, int r, int j) {
       if constexpr (RH == 1) return (acc[i][j] + acc[i][2 + j]) * f[0];
       else return acc[i][2 * r + j] * f[r];
     };
     auto slot = [&](int i, int r, int j) { return ((i * RH + r) * 2 + j) * 32 + lane; };
-    constexpr int ROUNDS = RH == 1 ? 2 : 4;  // warps add into the slices one after another
-    float* mine = mb + (RH == 1 ? (w & 1) * ROWS * DP : 0);
-    const int turn = RH == 1 ? 1 - (w >> 1) : kWarps - 1 - w;
+    if (idle) {
 #pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int r = 0; r < RH; ++r)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) *slice_at(w, slot(i, r, j)) = value(i, r, j);
+      __syncthreads();
+      return;
+    }
+    constexpr int ROUNDS = RH == 1 ? 2 : 4;
+    float* mine = mb + (RH == 1 ? (w & 1) * SLICE : 0);
+    const int turn = RH == 1 ? 1 - (w >> 1) : kWarps - 1 - w;
+#pragma unroll 1
     for (int k = 0; k < ROUNDS; ++k) {
       if (turn == k) {
 #pragma unroll
@@ -455,130 +476,155 @@ __global__ void __launch_bounds__(kWarps * 32) k_attend(AttendArgs a) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               float* p = mine + slot(i, r, j);
-              *p = k == 0 ? value(i, r, j) : *p + value(i, r, j);
+              *p = value(i, r, j) + (k == 0 ? 0.f : *p);
             }
       }
       __syncthreads();
     }
-    if (RH == 1) {
-      for (int i = threadIdx.x; i < ROWS * DP / 4; i += blockDim.x) {
-        float4 x = ((float4*)mb)[i];
-        const float4 y = ((float4*)(mb + ROWS * DP))[i];
-        x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
-        ((float4*)mb)[i] = x;
-      }
-      __syncthreads();
+  };
+  auto sum4 = [&](bool idle, int i) {  // floats 4 i .. 4 i + 3 of the sums
+    float4 x = *(const float4*)(idle ? slice_at(0, 4 * i) : mb + 4 * i);
+    auto add = [&](const float* p) {
+      const float4 y = *(const float4*)p;
+      x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+    };
+    if (idle) {
+#pragma unroll
+      for (int k = 1; k < kWarps; ++k) add(slice_at(k, 4 * i));
+    } else if (RH == 1) {
+      add(mb + SLICE + 4 * i);
     }
-    // mb: the item's sums relative to M; (M, L) of each row
-    float M = 0.f, L = 0.f;
-    if (threadIdx.x < ROWS) {
-      M = top_of(threadIdx.x);
+    return x;
+  };
+  // the output rows, from the sums and each row's (maximum, sum)
+  auto write_out = [&](bool idle, auto stat) {
+    const int kvh = cc.h / a.nhb, hb = cc.h % a.nhb;
+    const float vs = KV == MOE_DT_E4M3 && a.c.v_scale ? a.c.v_scale[kvh] : 1.f;
+    for (int u = threadIdx.x; u < KS * ROWS; u += blockDim.x) {
+      const int row = u % ROWS, p = u / ROWS;  // 16 values of one head
+      const int head = hb * ROWS + row;
+      if (head >= a.G || p * 16 >= a.c.D) continue;
+      const float2 st = stat(row);
+      const float k = st.y == 0.f ? 0.f : vs / st.y;
+      float o[16];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float4 x = sum4(idle, (((2 * p + i) * RH + (row >> 3)) * 2 + j) * 8 + (row & 7));
+          const float v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            // see the V fragments: with 8-bit values tile i holds the even or odd ones
+            const int d = KV == MOE_DT_E4M3 ? 4 * c + 2 * j + i : 8 * i + 2 * c + j;
+            o[d] = v[c] * k;
+          }
+        }
+      uint16_t* dst = (uint16_t*)a.out + cc.b * a.out_row +
+                      (int64_t)(kvh * a.G + head) * a.out_head + p * 16;
+      uint32_t pk[8];
+#pragma unroll
+      for (int d = 0; d < 8; ++d)
+        pk[d] = a.q_bf16 ? pack_bf16(o[2 * d], o[2 * d + 1]) : pack_f16(o[2 * d], o[2 * d + 1]);
+      ((uint4*)dst)[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+      ((uint4*)dst)[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+      if (p == 0 && a.lse)
+        a.lse[(int64_t)cc.b * a.Hq + kvh * a.G + head] = (st.x + log2f(st.y)) * (1.f / kLog2e);
+    }
+  };
+  // t0, t1: the tiles of the item that this run covered; first_u: the item's
+  // first tile among all; idle: the ring has nothing left to bring
+  auto end_item = [&](long long first_u, int t0, int t1, bool idle) {
+#pragma unroll
+    for (int r = 0; r < RH; ++r) {
+      l[r] += __shfl_xor_sync(~0u, l[r], 1);
+      l[r] += __shfl_xor_sync(~0u, l[r], 2);
+      if (c4 == 0) ml[w][r * 8 + g] = make_float2(m[r], l[r]);
+    }
+    __syncthreads();
+    auto stat = [&](int row) {  // (maximum, sum) of a row over the warps
+      float M = ml[0][row].x, L = 0.f;
+#pragma unroll
+      for (int i = 1; i < kWarps; ++i) M = fmaxf(M, ml[i][row].x);
 #pragma unroll
       for (int i = 0; i < kWarps; ++i)
-        L += ml[i][threadIdx.x].y * exp2_approx(ml[i][threadIdx.x].x - zero_if_empty(M));
+        L += ml[i][row].y * exp2_approx(ml[i][row].x - zero_if_empty(M));
+      return make_float2(M, L);
+    };
+    float f[RH];
+#pragma unroll
+    for (int r = 0; r < RH; ++r) f[r] = exp2_approx(m[r] - zero_if_empty(stat(r * 8 + g).x));
+    lay(idle, f);
+    if (t0 == 0 && t1 == cc.nt) {
+      write_out(idle, stat);
+      __syncthreads();
+      return;
+    }
+    // CTA c runs tiles [c U / ctas, (c + 1) U / ctas)
+    const int cs = (int)(((first_u + 1) * ctas - 1) / U);
+    const int np = (int)(((first_u + cc.nt) * ctas - 1) / U) - cs + 1;
+    auto part = [&](int p) { return a.parts + (size_t)(p == 0 ? 2 * cs + 1 : 2 * (cs + p)) * PART; };
+    float* to = part(blockIdx.x - cs);
+    for (int i = threadIdx.x; i < SLICE / 4; i += blockDim.x) ((float4*)to)[i] = sum4(idle, i);
+    if (threadIdx.x < ROWS) ((float2*)(to + SLICE))[threadIdx.x] = stat(threadIdx.x);
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      const unsigned done = atomicAdd(a.counters + cs, 1u);
+      is_last = done == (unsigned)np - 1;
+      if (is_last) a.counters[cs] = 0;
     }
     __syncthreads();
-    if (threadIdx.x < ROWS) ml[0][threadIdx.x] = make_float2(M, L);
-
-    bool write = t0 == 0 && t1 == cc.nt;
-    if (!write) {
-      // CTA c runs tiles [c U / ctas, (c + 1) U / ctas)
-      const int cs = (int)(((first_u + 1) * ctas - 1) / U);
-      const int ce = (int)(((first_u + cc.nt) * ctas - 1) / U);
-      const int np = ce - cs + 1;
-      auto part = [&](int p) { return a.parts + (size_t)(p == 0 ? 2 * cs + 1 : 2 * (cs + p)) * PART; };
-      float* to = part(blockIdx.x - cs);
-      for (int i = threadIdx.x; i < ROWS * DP / 4; i += blockDim.x)
-        ((float4*)to)[i] = ((float4*)mb)[i];
-      if (threadIdx.x < ROWS)
-        ((float2*)(to + ROWS * DP))[threadIdx.x] = make_float2(M, L);
-      __threadfence();
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        const unsigned done = atomicAdd(a.counters + cs, 1u);
-        is_last = done == (unsigned)np - 1;
-        if (is_last) a.counters[cs] = 0;
-      }
-      __syncthreads();
-      write = is_last;
-      if (write) {
-        __threadfence();
-        // (M, L) of each row over the parts: a share of them a thread, then over the threads
-        constexpr int Q = kWarps * 32 / ROWS;
-        M = __int_as_float(0xff800000), L = 0.f;
+    if (!is_last) return;
+    __threadfence();
+    // the last part has come: maximum and sum of each row over the parts (8 rows
+    // and 4 parts a step across a warp), then every warp adds each fourth part
+    float top_of[RH];
+#pragma unroll
+    for (int r = 0; r < RH; ++r) {
+      float M = __int_as_float(0xff800000), L = 0.f;
 #pragma unroll 4
-        for (int p = threadIdx.x / ROWS; p < np; p += Q) {
-          const float2 v = __ldcg((const float2*)(part(p) + ROWS * DP) + threadIdx.x % ROWS);
-          const float top = fmaxf(M, v.x);
-          L = L * exp2_approx(M - zero_if_empty(top)) + v.y * exp2_approx(v.x - zero_if_empty(top));
-          M = top;
-        }
-        joined[threadIdx.x] = make_float2(M, L);
-        __syncthreads();
-        if (threadIdx.x < ROWS) {
-#pragma unroll
-          for (int k = 1; k < Q; ++k) M = fmaxf(M, joined[k * ROWS + threadIdx.x].x);
-          L = 0.f;
-#pragma unroll
-          for (int k = 0; k < Q; ++k) {
-            const float2 v = joined[k * ROWS + threadIdx.x];
-            L += v.y * exp2_approx(v.x - zero_if_empty(M));
-          }
-          ml[0][threadIdx.x] = make_float2(M, L);
-        }
-        __syncthreads();
-        for (int i = threadIdx.x; i < ROWS * DP / 4; i += blockDim.x) {
-          const int row = (i & 7) + 8 * ((i / 16) % RH);
-          const float Mr = zero_if_empty(ml[0][row].x);
-          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-          for (int p = 0; p < np; ++p) {
-            const float* from = part(p);
-            const float4 y = __ldcg((const float4*)from + i);
-            const float e = exp2_approx(__ldcg((const float2*)(from + ROWS * DP) + row).x - Mr);
-            x.x += y.x * e, x.y += y.y * e, x.z += y.z * e, x.w += y.w * e;
-          }
-          ((float4*)mb)[i] = x;
-        }
+      for (int p = lane >> 3; p < np; p += 4) {
+        const float2 v = __ldcg((const float2*)(part(p) + SLICE) + r * 8 + (lane & 7));
+        const float top = fmaxf(M, v.x), z = zero_if_empty(top);
+        L = L * exp2_approx(M - z) + v.y * exp2_approx(v.x - z);
+        M = top;
       }
-    }
-    __syncthreads();
-    if (write) {
-      const float vs = KV == MOE_DT_E4M3 && a.c.v_scale ? a.c.v_scale[kvh] : 1.f;
-      for (int u = threadIdx.x; u < KS * ROWS; u += blockDim.x) {
-        const int row = u % ROWS, p = u / ROWS;  // 16 values of one head
-        const int head = hb * ROWS + row;
-        if (head >= a.G || p * 16 >= a.c.D) continue;
-        const float2 st = ml[0][row];
-        const float k = st.y == 0.f ? 0.f : vs / st.y;
-        float o[16];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const float4 x =
-                *(const float4*)(mb + (((2 * p + i) * RH + (row >> 3)) * 2 + j) * 32 + (row & 7) * 4);
-            const float v[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              // see the V fragments: with 8-bit values tile i holds the even or odd ones
-              const int d = KV == MOE_DT_E4M3 ? 4 * c + 2 * j + i : 8 * i + 2 * c + j;
-              o[d] = v[c] * k;
-            }
-          }
-        uint16_t* dst = (uint16_t*)a.out + cc.b * a.out_row +
-                        (int64_t)(kvh * a.G + head) * a.out_head + p * 16;
-        uint32_t pk[8];
-#pragma unroll
-        for (int d = 0; d < 8; ++d)
-          pk[d] = a.q_bf16 ? pack_bf16(o[2 * d], o[2 * d + 1]) : pack_f16(o[2 * d], o[2 * d + 1]);
-        ((uint4*)dst)[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-        ((uint4*)dst)[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
-        if (p == 0 && a.lse)
-          a.lse[(int64_t)cc.b * a.Hq + kvh * a.G + head] =
-              (st.x + log2f(st.y)) * (1.f / kLog2e);
+      for (int o = 8; o <= 16; o <<= 1) {
+        const float Mo = __shfl_xor_sync(~0u, M, o), Lo = __shfl_xor_sync(~0u, L, o);
+        const float top = fmaxf(M, Mo), z = zero_if_empty(top);
+        // the same order of the two in both lanes: the same bits
+        const float mine = L * exp2_approx(M - z), its = Lo * exp2_approx(Mo - z);
+        L = mine + its;
+        M = top;
       }
+      if (lane < 8 && w == 0) ml[0][r * 8 + lane] = make_float2(M, L);
+      top_of[r] = __shfl_sync(~0u, M, g);
     }
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+    for (int p = w; p < np; p += kWarps) {
+      const float* from = part(p);
+      float e[RH];
+#pragma unroll
+      for (int r = 0; r < RH; ++r)
+        e[r] = exp2_approx(__ldcg((const float2*)(from + SLICE) + r * 8 + g).x - zero_if_empty(top_of[r]));
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int r = 0; r < RH; ++r)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            acc[i][2 * r + j] += e[r] * __ldcg(from + ((i * RH + r) * 2 + j) * 32 + lane);
+    }
+    float one[RH];
+#pragma unroll
+    for (int r = 0; r < RH; ++r) one[r] = 1.f;
+    lay(idle, one);
+    write_out(idle, [&](int row) { return ml[0][row]; });
     __syncthreads();
   };
 
@@ -738,7 +784,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_attend(AttendArgs a) {
     stage = stage + 1 == S ? 0 : stage + 1;
     const bool done = cc.tile + 1 == cc.nt;
     if (done || u + 1 == u1) {
-      end_item(u - cc.tile, t0, cc.tile + 1);
+      end_item(u - cc.tile, t0, cc.tile + 1, u + 1 == u1);
       if (u + 1 < u1) {
         cc.next(a, nh);
         begin_item();
@@ -750,6 +796,10 @@ __global__ void __launch_bounds__(kWarps * 32) k_attend(AttendArgs a) {
   }
   cp_async_wait<0>();
 }
+
+// query heads taken at a time: 8 or 16; 16 rows of 256 values do not fit a
+// warp's registers beside the queries (more heads read the keys again, from L2)
+int rows_of(int G, int D) { return G <= 8 || D > 128 ? 8 : 16; }
 
 template <int KV, int DP, int RH>
 moe_status launch_attend(const AttendArgs& a, cudaStream_t s) {
@@ -776,14 +826,10 @@ moe_status launch_attend(const AttendArgs& a, cudaStream_t s) {
 template <int KV>
 moe_status pick_attend(const AttendArgs& a, cudaStream_t s) {
   const int D = a.c.D;
-  if (a.G <= 8) {
-    if (D <= 64) return launch_attend<KV, 64, 1>(a, s);
-    if (D <= 128) return launch_attend<KV, 128, 1>(a, s);
-    return launch_attend<KV, 256, 1>(a, s);
-  }
-  if (D <= 64) return launch_attend<KV, 64, 2>(a, s);
-  if (D <= 128) return launch_attend<KV, 128, 2>(a, s);
-  return launch_attend<KV, 256, 2>(a, s);
+  if (D > 128) return launch_attend<KV, 256, 1>(a, s);
+  if (rows_of(a.G, D) == 8)
+    return D <= 64 ? launch_attend<KV, 64, 1>(a, s) : launch_attend<KV, 128, 1>(a, s);
+  return D <= 64 ? launch_attend<KV, 64, 2>(a, s) : launch_attend<KV, 128, 2>(a, s);
 }
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
@@ -849,7 +895,7 @@ MOE_API moe_status kvcache_append(const kvcache_append_args* a, void* stream) {
 
 MOE_API size_t kvcache_attend_workspace_bytes(int Hq, int Hkv, int D) {
   if (Hq <= 0 || Hkv <= 0 || Hq % Hkv || D <= 0 || D > 256) return 0;
-  const size_t rows = Hq / Hkv <= 8 ? 8 : 16, dp = D <= 64 ? 64 : D <= 128 ? 128 : 256;
+  const size_t rows = rows_of(Hq / Hkv, D), dp = D <= 64 ? 64 : D <= 128 ? 128 : 256;
   return kCtlBytes + (size_t)kMaxCtas * 2 * rows * (dp + 2) * sizeof(float);
 }
 
@@ -870,7 +916,8 @@ MOE_API moe_status kvcache_attend(const kvcache_attend_args* a, void* stream) {
   AttendArgs k;
   k.c = a->c;
   k.B = a->B, k.Hq = a->Hq, k.G = a->Hq / a->c.Hkv;
-  k.nhb = k.G <= 8 ? 1 : (k.G + 15) / 16;
+  const int rows = rows_of(k.G, a->c.D);
+  k.nhb = (k.G + rows - 1) / rows;
   k.q = a->q, k.out = a->out, k.lse = a->lse;
   k.q_row = a->q_row, k.q_head = a->q_head, k.out_row = a->out_row, k.out_head = a->out_head;
   k.table_ld = a->table_ld, k.page_table = a->page_table, k.seq_lens = a->seq_lens;
