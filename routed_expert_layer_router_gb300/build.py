@@ -13,7 +13,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe.so")
 SOURCES = ["route.cu", "route_tc.cu", "permute.cu", "cache.cu", "decode.cu", "prefill.cu", "api.cu",
-           "noalloc.cu", "block_norm.cu", "kvcache.cu", "w4.cu"]
+           "noalloc.cu", "block_norm.cu", "kvcache.cu", "w4.cu", "w4_f16.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hidden",
          "-I" + INCLUDE, "-I" + CSRC]

@@ -143,33 +143,52 @@ __global__ void __launch_bounds__(kAppendThreads, 4) k_append(kvcache_append_arg
 
 // ------------------------------------------------------------------ attend
 // Bound by reading the cache once.  The sequences' tokens are cut into tiles
-// of 64 or 128; the tiles of all (sequence, kv head) items in a row are dealt to the
-// CTAs in equal contiguous runs, so a ragged batch and one long sequence fill
-// the GPU alike.  In a CTA each of 4 warps streams its 16 or 32 tokens of a tile through
-// its own ring of cp.async stages (no barrier between warps inside an item)
-// and keeps a running maximum, sum and output in registers.  The query heads
-// of a kv head are the rows of the matrix instructions, so K and V are read
-// once for all of them.  A run that covers an item writes its result; items
-// cut between CTAs leave their parts in the workspace, and the CTA that
-// finishes last adds them in run order (the same bits every time).
+// of 64 or 128; the tiles of all (sequence, kv head) items in a row are dealt to
+// the CTAs in equal contiguous runs, so a ragged batch and one long sequence fill
+// the GPU alike.  In a CTA each of 4 warps streams its 16 or 32 tokens of a tile
+// through its own ring of cp.async stages (a token's place in its page is found
+// for each token, so pages of any size run alike; no barrier between warps inside
+// an item) and keeps a running maximum, sum and output in registers.  The query heads of a kv head are the rows of the matrix
+// instructions, so K and V are read once for all of them.  A run that covers an
+// item writes its result; items cut between CTAs leave their parts in the
+// workspace, and the CTA that finishes last adds them (in an order of the parts,
+// so the same bits every time).
+// (TMA boxes of a page's tokens, one per warp and stage, were measured slower:
+// 98 against 86 us at 1 x 131075 tokens of 8 x 128 values in bf16.)
 constexpr int kWarps = 4;
-constexpr int kMaxCtas = 2 * kSMs;
+constexpr int kMaxCtas = 3 * kSMs;
 constexpr size_t kCtlBytes = 4096;  // one counter a CTA
 static_assert(kMaxCtas * sizeof(unsigned) <= kCtlBytes, "counters");
 constexpr float kLog2e = 1.4426950408889634f;
+#define NEG_INF __int_as_float(0xff800000)
 
-template <int KV, int DP>
+template <int KV, int DP, int RH>
 struct Ring {
   static constexpr int ES = KV == MOE_DT_E4M3 ? 1 : 2;
-  static constexpr int RB = DP * ES;             // bytes of a token's row
+  static constexpr int RB = DP * ES;               // bytes of a token's row
   static constexpr int TOK = RB <= 128 ? 32 : 16;  // tokens of a warp's stage: 8 KB where it can
   static constexpr int TILE = kWarps * TOK;
   static constexpr int WARP = 2 * TOK * RB;        // one stage of one warp: K and V
   static constexpr int STAGE = kWarps * WARP;
-  // about 96 KB a CTA, so that two share an SM and ~128 KB an SM are in
-  // flight; 256-value rows of 16 bits take 3 stages and the SM alone
-  static constexpr int S = 98304 / STAGE < 3 ? 3 : (98304 / STAGE > 6 ? 6 : 98304 / STAGE);
+  // CTAs of an SM and their stages.  Rows of up to 128 bytes take most work a byte:
+  // three CTAs of 64 KB, whose 12 warps hide each other's latencies (97 against
+  // 102 us at two of 96 KB, 32 ragged sequences in 8 bits); with 16 rows, whose
+  // registers leave room for two, and at 256 bytes, where bytes under way count
+  // for more (86 against 95 us, one long sequence in bf16), two of 96 KB.
+  static constexpr int CTAS = RB == 512 ? 1 : RB <= 128 && RH == 1 ? 3 : 2;
+  static constexpr int S = RB == 512 || (RB == 256 && ES == 2) ? 3
+                           : CTAS == 3 || DP == 256            ? 65536 / STAGE
+                                                               : 98304 / STAGE;
+  // a tile's loads are issued before the work on the tile S - 1 earlier, or, with two
+  // stages, after that on the tile S earlier (86 against 92 us where there are three)
+  static constexpr bool EARLY = S > 2;
   static constexpr int BYTES = S * STAGE;
+  // 16-byte chunk `ch` of row `row`, placed so that 8 rows' same chunk lie in 8
+  // different bank groups
+  static __device__ __forceinline__ uint32_t at(int row, int ch) {
+    if constexpr (RB == 64) return row * RB + ((ch ^ (row >> 1)) & 3) * 16;
+    else return row * RB + (ch ^ (row & 7)) * 16;
+  }
 };
 
 struct AttendArgs {
@@ -181,32 +200,30 @@ struct AttendArgs {
   int64_t q_row, q_head, out_row, out_head, table_ld;
   const int32_t* page_table;
   const int32_t* seq_lens;
-  int max_pages, window, q_bf16;
-  uint32_t div_mul, div_shift;  // position -> page column
+  int cap, window, q_bf16;
+  uint32_t div_mul, div_shift;   // position -> page column
   float scale, softcap;
   unsigned* counters;
   float* parts;
   int32_t* status;
 };
 
-// tiles of sequence b: its window is [start, start + n)
+// positions [start, end) of sequence b that are read
 struct Span {
-  int start, n;
+  int start, end;
 };
-__device__ __forceinline__ int page_column(const AttendArgs& a, int pos) {
-  // floor(pos / page_size) for pos < 2^31 (multiplier from the host)
-  return (int)(((uint64_t)(uint32_t)pos * a.div_mul) >> a.div_shift);
-}
 __device__ __forceinline__ Span span_of(const AttendArgs& a, int b) {
   const int len0 = a.seq_lens[b];
-  const int64_t cap64 = (int64_t)a.max_pages * a.c.page_size;
-  const int cap = cap64 > 0x7fffff00 ? 0x7fffff00 : (int)cap64;  // tiles stay within int
-  const int len = min(max(len0, 0), cap);
+  const int len = min(max(len0, 0), a.cap);
   if (len != len0) set_status(a.status, MOE_ERR_DEVICE);
   Span s;
+  s.end = len;
   s.start = a.window > 0 && len > a.window ? len - a.window : 0;
-  s.n = len - s.start;
   return s;
+}
+template <int TILE>
+__device__ __forceinline__ int tiles_of(const Span& s) {
+  return (s.end - s.start + TILE - 1) / TILE;
 }
 
 // walks tiles in (sequence, head block, tile) order
@@ -222,26 +239,21 @@ struct Cursor {
     do {
       if (++b >= a.B) return;
       s = span_of(a, b);
-      nt = (s.n + TILE - 1) / TILE;
+      nt = tiles_of<TILE>(s);
     } while (nt == 0);
   }
 };
 
-template <int RB>
-__device__ __forceinline__ uint32_t swz(int row, int ch) {
-  // 16-byte chunk `ch` of a row, placed so that 8 rows' same chunk lie in 8
-  // different bank groups
-  if constexpr (RB == 64) return row * RB + ((ch ^ (row >> 1)) & 3) * 16;
-  else return row * RB + (ch ^ (row & 7)) * 16;
-}
-
 template <int KV, int DP, int RH>
-__global__ void __launch_bounds__(kWarps * 32) k_attend(AttendArgs a) {
-  using R = Ring<KV, DP>;
+__global__ void __launch_bounds__(kWarps * 32, Ring<KV, DP, RH>::CTAS) k_attend(AttendArgs a) {
+  using R = Ring<KV, DP, RH>;
   constexpr int MT = KV == MOE_DT_BF16 ? MOE_DT_BF16 : MOE_DT_F16;  // operands' type
-  constexpr int RB = R::RB, CPR = RB / 16, S = R::S, KS = DP / 16, NT = DP / 8;
+  constexpr int RB = R::RB, CPR = RB / 16, S = R::S, AHEAD = R::EARLY ? S - 1 : S;
+  constexpr int KS = DP / 16, NT = DP / 8;
   constexpr int TOK = R::TOK, TILE = R::TILE, TT = TOK / 8;  // TT: score tiles of 8 tokens
-  constexpr int ROWS = 8 * RH, PART = ROWS * (DP + 2);
+  constexpr int ROWS = 8 * RH, SLICE = ROWS * DP, PART = ROWS * (DP + 2);
+  constexpr uint32_t ALL = TOK == 32 ? ~0u : 0xffffu;
+  static_assert(SLICE * 4 <= R::WARP, "a warp's sums fit its part of a stage");
   extern __shared__ __align__(128) uint8_t ring[];
   float* mb = (float*)(ring + R::BYTES);  // merge buffer: RH 1: two slices of 8 rows, 2: one of 16
   __shared__ float2 ml[kWarps][ROWS];
@@ -253,72 +265,73 @@ __global__ void __launch_bounds__(kWarps * 32) k_attend(AttendArgs a) {
   pdl_wait();
   pdl_launch_dependents();
 
-  // rows without tokens: zeros, while this CTA's first loads are under way
+  // ---- this CTA's run [u0, u1) of the U tiles: U / ctas each, the first U % ctas
+  // one more.  A CTA more costs an item's join another part, a tile more costs its
+  // CTA the tile: runs of at least about sqrt(n / 2) tiles for items of n.
+  Span s0 = {0, 0};
+  if (lane < a.B) s0 = span_of(a, lane);
+  const int n0 = tiles_of<TILE>(s0);
+  int U = n0, longest = n0;
+  bool idle_rows = lane < a.B && n0 == 0;
+  for (int b = lane + 32; b < a.B; b += 32) {
+    const int t = tiles_of<TILE>(span_of(a, b));
+    U += t;
+    longest = max(longest, t);
+    idle_rows |= t == 0;
+  }
+  U = __reduce_add_sync(~0u, U) * nh;
+  longest = __reduce_max_sync(~0u, longest);
+  const int run = max(1, (int)sqrtf(0.5f * longest));
+  const int ctas = min((U + run - 1) / run, (int)gridDim.x);
+  const int each = ctas ? U / ctas : 0, more = U - each * ctas;
+  // rows without tokens: zeros
   auto zero_rows = [&]() {
+    if (!__any_sync(~0u, idle_rows)) return;
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-      if (span_of(a, b).n > 0) continue;
+      const Span s = span_of(a, b);
+      if (s.end > s.start) continue;
       const int per = a.c.D / 8;
       for (int i = threadIdx.x; i < a.Hq * per; i += blockDim.x)
         *(uint4*)((uint16_t*)a.out + b * a.out_row + (i / per) * a.out_head + (i % per) * 8) =
             make_uint4(0, 0, 0, 0);
       if (a.lse)
         for (int i = threadIdx.x; i < a.Hq; i += blockDim.x)
-          a.lse[(int64_t)b * a.Hq + i] = __int_as_float(0xff800000);
+          a.lse[(int64_t)b * a.Hq + i] = NEG_INF;
     }
   };
-
-  // this CTA's run [u0, u1) of the U tiles
-  auto tiles_of = [](const Span& s) { return (s.n + TILE - 1) / TILE; };
-  Span s0 = {0, 0};
-  if (lane < a.B) s0 = span_of(a, lane);
-  int most = tiles_of(s0);
-  long long U = most;
-  for (int b = lane + 32; b < a.B; b += 32) {
-    const int t = tiles_of(span_of(a, b));
-    U += t;
-    most = max(most, t);
-  }
-  const int longest = __reduce_max_sync(~0u, most);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) U += __shfl_xor_sync(~0u, U, o);
-  U *= nh;
-  // A CTA more costs an item's join another part, a tile more costs its CTA the
-  // tile: runs of about sqrt(n / 2) tiles for items of n, unless the GPU is full
-  int run = 1;
-  while (2 * (run + 1) * (run + 1) <= longest) ++run;
-  const long long want = (U + run - 1) / run;
-  const long long ctas = want < gridDim.x ? want : gridDim.x;
-  if (blockIdx.x >= ctas) {
+  if ((int)blockIdx.x >= ctas) {
     zero_rows();
     return;
   }
-  const long long u0 = blockIdx.x * U / ctas, u1 = (blockIdx.x + 1) * U / ctas;
+  const int cta = blockIdx.x;
+  const int u0 = cta * each + min(cta, more), u1 = u0 + each + (cta < more);
   Cursor<TILE> ci = {};
   {
-    long long rem = u0;
-    for (int base = 0; base < a.B; base += 32) {
+    int rem = u0;
+#pragma unroll 1
+    for (int first = 0; first < a.B; first += 32) {
       Span s = s0;
-      if (base) {
+      if (first) {
         s = {0, 0};
-        if (base + lane < a.B) s = span_of(a, base + lane);
+        if (first + lane < a.B) s = span_of(a, first + lane);
       }
-      const long long mine = (long long)tiles_of(s) * nh;
-      long long incl = mine;
+      const int mine = tiles_of<TILE>(s) * nh;
+      int incl = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(~0u, incl, o);
-        if (lane >= o) incl += v;
+        const int x = __shfl_up_sync(~0u, incl, o);
+        if (lane >= o) incl += x;
       }
       const uint32_t over = __ballot_sync(~0u, incl > rem);
       if (over) {
         const int src = __ffs(over) - 1;
         rem -= __shfl_sync(~0u, incl - mine, src);
-        ci.b = base + src;
+        ci.b = first + src;
         ci.s.start = __shfl_sync(~0u, s.start, src);
-        ci.s.n = __shfl_sync(~0u, s.n, src);
-        ci.nt = tiles_of(ci.s);
-        ci.h = (int)(rem / ci.nt);
-        ci.tile = (int)(rem % ci.nt);
+        ci.s.end = __shfl_sync(~0u, s.end, src);
+        ci.nt = tiles_of<TILE>(ci.s);
+        ci.h = rem / ci.nt;
+        ci.tile = rem - ci.h * ci.nt;
         break;
       }
       rem -= __shfl_sync(~0u, incl, 31);
@@ -326,31 +339,32 @@ __global__ void __launch_bounds__(kWarps * 32) k_attend(AttendArgs a) {
   }
   Cursor<TILE> cc = ci;  // ci issues loads ahead of cc, which computes
 
+  // ---- loads: lane i knows the place of token i of the warp's next stage
   const uint32_t base = ptx::smem_u32(ring) + w * R::WARP;
   const int nch = a.c.D * R::ES / 16;
-  // the page of this lane's token of the tile that is issued next
-  auto page_of = [&](const Cursor<TILE>& k) {
-    const int rel = k.tile * TILE + w * TOK + (lane & (TOK - 1));
-    if (rel >= k.s.n) return -1;
-    return a.page_table[(int64_t)k.b * a.table_ld + page_column(a, k.s.start + rel)];
+  auto page_column = [&](int pos) {  // floor(pos / page_size) (multiplier from the host)
+    return (int)(((uint64_t)(uint32_t)pos * a.div_mul) >> a.div_shift);
   };
-  int page = page_of(ci);
-  long long ui = u0;
+  auto page_of = [&](const Cursor<TILE>& k) {
+    const int pos = k.s.start + k.tile * TILE + w * TOK + (lane & (TOK - 1));
+    return pos < k.s.end ? a.page_table[k.b * a.table_ld + page_column(pos)] : -1;
+  };
+  int ui = u0, page;       // next tile to issue, and this lane's page of it
+  Cursor<TILE> cp = ci;    // the next tile whose page is asked for
   auto issue = [&](int stage) {
     if (ui < u1) {
-      const int rel = ci.tile * TILE + w * TOK + (lane & (TOK - 1));
-      const int pos = ci.s.start + rel;
-      bool ok = rel < ci.s.n;
+      const int pos = ci.s.start + ci.tile * TILE + w * TOK + (lane & (TOK - 1));
+      bool ok = pos < ci.s.end;
       if (ok && (page < 0 || page >= a.c.n_pages)) {
         set_status(a.status, MOE_ERR_DEVICE);
         ok = false;
       }
-      const int at = pos - page_column(a, pos) * a.c.page_size;
+      const int slot = pos - page_column(pos) * a.c.page_size;
       const int64_t off = ok ? ((int64_t)page * a.c.page_stride +
                                 (int64_t)(ci.h / a.nhb) * a.c.head_stride +
-                                (int64_t)at * a.c.token_stride) * R::ES
+                                (int64_t)slot * a.c.token_stride) * R::ES
                              : 0;
-      const uint32_t mask = __ballot_sync(~0u, ok) & (TOK == 32 ? ~0u : 0xffffu);
+      const uint32_t mask = __ballot_sync(~0u, ok) & ALL;
       if (lane == 0) valid[w][stage] = mask;
       const uint32_t kd = base + stage * R::STAGE, vd = kd + TOK * RB;
 #pragma unroll
@@ -358,19 +372,17 @@ __global__ void __launch_bounds__(kWarps * 32) k_attend(AttendArgs a) {
         const int idx = i * 32 + lane, row = idx / CPR, ch = idx % CPR;
         const int64_t o = __shfl_sync(~0u, off, row) + ch * 16;
         const bool v = ((mask >> row) & 1) && ch < nch;
-        const uint32_t d = swz<RB>(row, ch);
+        const uint32_t d = R::at(row, ch);
         cp_async16(kd + d, (const uint8_t*)a.c.k_pages + (v ? o : 0), v ? 16 : 0);
         cp_async16(vd + d, (const uint8_t*)a.c.v_pages + (v ? o : 0), v ? 16 : 0);
       }
       ++ui;
-      if (ui < u1) {
-        ci.next(a, nh);
-        page = page_of(ci);
-      }
+      if (ui < u1) ci.next(a, nh);
     }
     cp_async_commit();
   };
 
+  // ---- queries of an item, as matrix operands
   uint32_t qa[KS][2 * RH];
   float acc[NT][4], m[RH], l[RH], sc[RH];
   auto begin_item = [&]() {
@@ -378,11 +390,11 @@ __global__ void __launch_bounds__(kWarps * 32) k_attend(AttendArgs a) {
     for (int i = 0; i < NT; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-    const int kvh = cc.h / a.nhb, hb = cc.h % a.nhb;
+    const int kvh = cc.h / a.nhb, hb = cc.h - kvh * a.nhb;
     const float ks = KV == MOE_DT_E4M3 && a.c.k_scale ? a.c.k_scale[kvh] : 1.f;
 #pragma unroll
     for (int r = 0; r < RH; ++r) {
-      m[r] = __int_as_float(0xff800000);
+      m[r] = NEG_INF;
       l[r] = 0.f;
       const int row = hb * ROWS + r * 8 + g;
       const bool on = row < a.G;
@@ -434,114 +446,10 @@ __global__ void __launch_bounds__(kWarps * 32) k_attend(AttendArgs a) {
     }
   };
 
-  // ---- the end of an item
-  auto zero_if_empty = [](float M) { return M == __int_as_float(0xff800000) ? 0.f : M; };
-  // Scaled sums of the warps meet in shared memory, in the fragments' order:
-  // value (n tile i, row half r, column j) of a lane at ((i RH + r) 2 + j) 32 +
-  // lane.  Once the ring has nothing left to bring (`idle`), each warp lays its
-  // sums into its own part of it; otherwise the warps add into the merge buffer
-  // (two slices of 8 rows, one of 16) one after another.
-  constexpr int SLICE = ROWS * DP;
-  auto slice_at = [&](int warp, int off) {  // of the ring: float `off` of a warp's slice
-    const int b = off * 4;
-    return (float*)(ring + (b / R::WARP) * R::STAGE + warp * R::WARP + b % R::WARP);
-  };
-  static_assert(SLICE * 4 <= S * R::WARP, "a warp's sums fit its ring");
-  auto lay = [&](bool idle, const float (&f)[RH]) {
-    auto value = [&](int i, int r, int j) {
-      if constexpr (RH == 1) return (acc[i][j] + acc[i][2 + j]) * f[0];
-      else return acc[i][2 * r + j] * f[r];
-    };
-    auto slot = [&](int i, int r, int j) { return ((i * RH + r) * 2 + j) * 32 + lane; };
-    if (idle) {
-#pragma unroll
-      for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int r = 0; r < RH; ++r)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) *slice_at(w, slot(i, r, j)) = value(i, r, j);
-      __syncthreads();
-      return;
-    }
-    constexpr int ROUNDS = RH == 1 ? 2 : 4;
-    float* mine = mb + (RH == 1 ? (w & 1) * SLICE : 0);
-    const int turn = RH == 1 ? 1 - (w >> 1) : kWarps - 1 - w;
-#pragma unroll 1
-    for (int k = 0; k < ROUNDS; ++k) {
-      if (turn == k) {
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-          for (int r = 0; r < RH; ++r)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              float* p = mine + slot(i, r, j);
-              *p = value(i, r, j) + (k == 0 ? 0.f : *p);
-            }
-      }
-      __syncthreads();
-    }
-  };
-  auto sum4 = [&](bool idle, int i) {  // floats 4 i .. 4 i + 3 of the sums
-    float4 x = *(const float4*)(idle ? slice_at(0, 4 * i) : mb + 4 * i);
-    auto add = [&](const float* p) {
-      const float4 y = *(const float4*)p;
-      x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
-    };
-    if (idle) {
-#pragma unroll
-      for (int k = 1; k < kWarps; ++k) add(slice_at(k, 4 * i));
-    } else if (RH == 1) {
-      add(mb + SLICE + 4 * i);
-    }
-    return x;
-  };
-  // the output rows, from the sums and each row's (maximum, sum)
-  auto write_out = [&](bool idle, auto stat) {
-    const int kvh = cc.h / a.nhb, hb = cc.h % a.nhb;
-    const float vs = KV == MOE_DT_E4M3 && a.c.v_scale ? a.c.v_scale[kvh] : 1.f;
-    for (int u = threadIdx.x; u < KS * ROWS; u += blockDim.x) {
-      const int row = u % ROWS, p = u / ROWS;  // 16 values of one head
-      const int head = hb * ROWS + row;
-      if (head >= a.G || p * 16 >= a.c.D) continue;
-      const float2 st = stat(row);
-      const float k = st.y == 0.f ? 0.f : vs / st.y;
-      float o[16];
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float4 x = sum4(idle, (((2 * p + i) * RH + (row >> 3)) * 2 + j) * 8 + (row & 7));
-          const float v[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            // see the V fragments: with 8-bit values tile i holds the even or odd ones
-            const int d = KV == MOE_DT_E4M3 ? 4 * c + 2 * j + i : 8 * i + 2 * c + j;
-            o[d] = v[c] * k;
-          }
-        }
-      uint16_t* dst = (uint16_t*)a.out + cc.b * a.out_row +
-                      (int64_t)(kvh * a.G + head) * a.out_head + p * 16;
-      uint32_t pk[8];
-#pragma unroll
-      for (int d = 0; d < 8; ++d)
-        pk[d] = a.q_bf16 ? pack_bf16(o[2 * d], o[2 * d + 1]) : pack_f16(o[2 * d], o[2 * d + 1]);
-      ((uint4*)dst)[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-      ((uint4*)dst)[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
-      if (p == 0 && a.lse)
-        a.lse[(int64_t)cc.b * a.Hq + kvh * a.G + head] = (st.x + log2f(st.y)) * (1.f / kLog2e);
-    }
-  };
-  // t0, t1: the tiles of the item that this run covered; first_u: the item's
-  // first tile among all; idle: the ring has nothing left to bring
-  auto end_item = [&](long long first_u, int t0, int t1, bool idle) {
-#pragma unroll
-    for (int r = 0; r < RH; ++r) {
-      l[r] += __shfl_xor_sync(~0u, l[r], 1);
-      l[r] += __shfl_xor_sync(~0u, l[r], 2);
-      if (c4 == 0) ml[w][r * 8 + g] = make_float2(m[r], l[r]);
-    }
-    __syncthreads();
+  // ---- the end of an item: t0, t1: the tiles of it that this run covered; first_u:
+  // its first tile among all; idle: the ring has nothing left to bring
+  auto zero_if_empty = [](float M) { return M == NEG_INF ? 0.f : M; };
+  auto end_item = [&](int first_u, int t0, int t1, bool idle) {
     auto stat = [&](int row) {  // (maximum, sum) of a row over the warps
       float M = ml[0][row].x, L = 0.f;
 #pragma unroll
@@ -551,96 +459,191 @@ __global__ void __launch_bounds__(kWarps * 32) k_attend(AttendArgs a) {
         L += ml[i][row].y * exp2_approx(ml[i][row].x - zero_if_empty(M));
       return make_float2(M, L);
     };
-    float f[RH];
+    // The warps' scaled sums meet in shared memory, in the fragments' order: value
+    // (n tile i, row half r, column j) of a lane at ((i RH + r) 2 + j) 32 + lane.
+    // Once the ring is idle each warp lays them into its own part of it;
+    // otherwise the warps add into the merge buffer one after another.
+    const int rounds = idle ? 1 : RH == 1 ? 2 : 4;
+    const int turn = idle ? 0 : RH == 1 ? 1 - (w >> 1) : kWarps - 1 - w;
+    float* mine = idle ? (float*)(ring + w * R::WARP) : mb + (RH == 1 ? (w & 1) * SLICE : 0);
+    const float* slices = idle ? (const float*)ring : mb;
+    const int nslice = idle ? kWarps : RH == 1 ? 2 : 1, pitch = idle ? R::WARP / 4 : SLICE;
+    auto sum4 = [&](int i) {  // floats 4 i .. 4 i + 3 of the sums
+      float4 x = *(const float4*)(slices + 4 * i);
 #pragma unroll
-    for (int r = 0; r < RH; ++r) f[r] = exp2_approx(m[r] - zero_if_empty(stat(r * 8 + g).x));
-    lay(idle, f);
-    if (t0 == 0 && t1 == cc.nt) {
-      write_out(idle, stat);
-      __syncthreads();
-      return;
-    }
-    // CTA c runs tiles [c U / ctas, (c + 1) U / ctas)
-    const int cs = (int)(((first_u + 1) * ctas - 1) / U);
-    const int np = (int)(((first_u + cc.nt) * ctas - 1) / U) - cs + 1;
-    auto part = [&](int p) { return a.parts + (size_t)(p == 0 ? 2 * cs + 1 : 2 * (cs + p)) * PART; };
-    float* to = part(blockIdx.x - cs);
-    for (int i = threadIdx.x; i < SLICE / 4; i += blockDim.x) ((float4*)to)[i] = sum4(idle, i);
-    if (threadIdx.x < ROWS) ((float2*)(to + SLICE))[threadIdx.x] = stat(threadIdx.x);
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      const unsigned done = atomicAdd(a.counters + cs, 1u);
-      is_last = done == (unsigned)np - 1;
-      if (is_last) a.counters[cs] = 0;
-    }
-    __syncthreads();
-    if (!is_last) return;
-    __threadfence();
-    // the last part has come: maximum and sum of each row over the parts (8 rows
-    // and 4 parts a step across a warp), then every warp adds each fourth part
-    float top_of[RH];
+      for (int k = 1; k < kWarps; ++k) {
+        if (k >= nslice) break;
+        const float4 y = *(const float4*)(slices + k * pitch + 4 * i);
+        x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+      }
+      return x;
+    };
+    const int kvh = cc.h / a.nhb, hb = cc.h - kvh * a.nhb;
 #pragma unroll
     for (int r = 0; r < RH; ++r) {
-      float M = __int_as_float(0xff800000), L = 0.f;
-#pragma unroll 4
-      for (int p = lane >> 3; p < np; p += 4) {
-        const float2 v = __ldcg((const float2*)(part(p) + SLICE) + r * 8 + (lane & 7));
-        const float top = fmaxf(M, v.x), z = zero_if_empty(top);
-        L = L * exp2_approx(M - z) + v.y * exp2_approx(v.x - z);
-        M = top;
-      }
-#pragma unroll
-      for (int o = 8; o <= 16; o <<= 1) {
-        const float Mo = __shfl_xor_sync(~0u, M, o), Lo = __shfl_xor_sync(~0u, L, o);
-        const float top = fmaxf(M, Mo), z = zero_if_empty(top);
-        // the same order of the two in both lanes: the same bits
-        const float mine = L * exp2_approx(M - z), its = Lo * exp2_approx(Mo - z);
-        L = mine + its;
-        M = top;
-      }
-      if (lane < 8 && w == 0) ml[0][r * 8 + lane] = make_float2(M, L);
-      top_of[r] = __shfl_sync(~0u, M, g);
+      l[r] += __shfl_xor_sync(~0u, l[r], 1);
+      l[r] += __shfl_xor_sync(~0u, l[r], 2);
     }
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-    for (int p = w; p < np; p += kWarps) {
-      const float* from = part(p);
-      float e[RH];
+#pragma unroll 1
+    for (bool whole = t0 == 0 && t1 == cc.nt;; whole = true) {
 #pragma unroll
       for (int r = 0; r < RH; ++r)
-        e[r] = exp2_approx(__ldcg((const float2*)(from + SLICE) + r * 8 + g).x - zero_if_empty(top_of[r]));
+        if (c4 == 0) ml[w][r * 8 + g] = make_float2(m[r], l[r]);
+      __syncthreads();
+      float f[RH];
+#pragma unroll
+      for (int r = 0; r < RH; ++r) f[r] = exp2_approx(m[r] - zero_if_empty(stat(r * 8 + g).x));
+#pragma unroll 1
+      for (int k = 0; k < rounds; ++k) {
+        if (turn == k) {
+#pragma unroll
+          for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int r = 0; r < RH; ++r)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                float* p = mine + ((i * RH + r) * 2 + j) * 32 + lane;
+                const float v = RH == 1 ? (acc[i][j] + acc[i][2 + j]) * f[0] : acc[i][2 * r + j] * f[r];
+                *p = k ? *p + v : v;
+              }
+        }
+        __syncthreads();
+      }
+      if (whole) {
+        const float vs = KV == MOE_DT_E4M3 && a.c.v_scale ? a.c.v_scale[kvh] : 1.f;
+#pragma unroll 1
+        for (int u = threadIdx.x; u < KS * ROWS; u += blockDim.x) {
+          const int row = u % ROWS, p = u / ROWS;  // 16 values of one head
+          const int head = hb * ROWS + row;
+          if (head >= a.G || p * 16 >= a.c.D) continue;
+          const float2 st = stat(row);
+          const float k = st.y == 0.f ? 0.f : vs / st.y;
+          float o[16];
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float4 x = sum4((((2 * p + i) * RH + (row >> 3)) * 2 + j) * 8 + (row & 7));
+              const float v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                // see the V fragments: with 8-bit values tile i holds the even or odd ones
+                const int d = KV == MOE_DT_E4M3 ? 4 * c + 2 * j + i : 8 * i + 2 * c + j;
+                o[d] = v[c] * k;
+              }
+            }
+          uint16_t* dst = (uint16_t*)a.out + cc.b * a.out_row +
+                          (int64_t)(kvh * a.G + head) * a.out_head + p * 16;
+          uint32_t pk[8];
+#pragma unroll
+          for (int d = 0; d < 8; ++d)
+            pk[d] = a.q_bf16 ? pack_bf16(o[2 * d], o[2 * d + 1]) : pack_f16(o[2 * d], o[2 * d + 1]);
+          ((uint4*)dst)[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+          ((uint4*)dst)[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+          if (p == 0 && a.lse)
+            a.lse[(int64_t)cc.b * a.Hq + kvh * a.G + head] = (st.x + log2f(st.y)) * (1.f / kLog2e);
+        }
+        __syncthreads();
+        return;
+      }
+      // part p of the item comes from run cs + p; the first is that run's last
+      // piece, any other its run's first
+      auto run_of = [&](int u) {
+        const int longer = more * (each + 1);
+        return u < longer ? u / (each + 1) : more + (u - longer) / each;
+      };
+      const int cs = run_of(first_u), np = run_of(first_u + cc.nt - 1) - cs + 1;
+      auto part = [&](int p) {
+        return a.parts + (size_t)(p == 0 ? 2 * cs + 1 : 2 * (cs + p)) * PART;
+      };
+      float* to = part(cta - cs);
+#pragma unroll 1
+      for (int i = threadIdx.x; i < SLICE / 4; i += blockDim.x) ((float4*)to)[i] = sum4(i);
+      if (threadIdx.x < ROWS) ((float2*)(to + SLICE))[threadIdx.x] = stat(threadIdx.x);
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        // releases the CTA's part, which the barrier has gathered, and takes the others'
+        unsigned done;
+        asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;"
+                     : "=r"(done)
+                     : "l"(a.counters + cs)
+                     : "memory");
+        is_last = done == (unsigned)np - 1;
+        if (is_last) a.counters[cs] = 0;
+      }
+      __syncthreads();
+      if (!is_last) return;
+      // The last part has come.  Each warp adds every fourth part to its registers
+      // under a running maximum, so that all loads leave at once; the warps then
+      // meet as before.
 #pragma unroll
       for (int i = 0; i < NT; ++i)
 #pragma unroll
-        for (int r = 0; r < RH; ++r)
+        for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
-            acc[i][2 * r + j] += e[r] * __ldcg(from + ((i * RH + r) * 2 + j) * 32 + lane);
+      for (int r = 0; r < RH; ++r) m[r] = NEG_INF, l[r] = 0.f;
+#pragma unroll 1
+      for (int p = w; p < np; p += kWarps) {
+        const float* from = part(p);
+        float v[NT][RH][2];
+        float2 st[RH];
+#pragma unroll
+        for (int r = 0; r < RH; ++r) st[r] = __ldcg((const float2*)(from + SLICE) + r * 8 + g);
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int r = 0; r < RH; ++r)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              v[i][r][j] = __ldcg(from + ((i * RH + r) * 2 + j) * 32 + lane);
+#pragma unroll
+        for (int r = 0; r < RH; ++r) {
+          const float top = fmaxf(m[r], st[r].x), z = zero_if_empty(top);
+          const float old = exp2_approx(m[r] - z), e = exp2_approx(st[r].x - z);
+          m[r] = top;
+          l[r] = l[r] * old + st[r].y * e;
+#pragma unroll
+          for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              acc[i][2 * r + j] = acc[i][2 * r + j] * old + e * v[i][r][j];
+        }
+      }
     }
-    float one[RH];
-#pragma unroll
-    for (int r = 0; r < RH; ++r) one[r] = 1.f;
-    lay(idle, one);
-    write_out(idle, [&](int row) { return ml[0][row]; });
-    __syncthreads();
   };
 
-  begin_item();
+  {
+    int pages[AHEAD + 1];  // of the first tiles: the loads leave together
 #pragma unroll
-  for (int i = 0; i < S - 1; ++i) issue(i);
-  zero_rows();
-  int t0 = cc.tile;
-  int stage = 0;
-  for (long long u = u0; u < u1; ++u) {
-    cp_async_wait<S - 2>();
-    __syncwarp();
-    {
-      const int to = stage == 0 ? S - 1 : stage - 1;
-      issue(to);
+    for (int i = 0; i <= AHEAD; ++i) {
+      pages[i] = -1;
+      if (u0 + i < u1) {
+        pages[i] = page_of(cp);
+        if (u0 + i + 1 < u1) cp.next(a, nh);
+      }
     }
+    begin_item();
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      page = pages[i];
+      issue(i);
+    }
+    page = pages[AHEAD];
+  }
+  auto issue_next = [&](int stage) {
+    issue(stage);
+    if (ui < u1) {
+      page = page_of(cp);
+      if (ui + 1 < u1) cp.next(a, nh);
+    }
+  };
+  zero_rows();
+  int t0 = cc.tile, stage = 0;
+#pragma unroll 1
+  for (int u = u0; u < u1; ++u) {
+    cp_async_wait<AHEAD - 1>();
+    __syncwarp();
+    if (R::EARLY) issue_next(stage == 0 ? S - 1 : stage - 1);
     const uint32_t kd = base + stage * R::STAGE, vd = kd + TOK * RB;
     const uint32_t mask = valid[w][stage];
 
@@ -652,7 +655,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_attend(AttendArgs a) {
 #pragma unroll
         for (int k = 0; k < KS; k += 2) {
           uint32_t r[4];
-          ldmatrix_x4(r, kd + swz<RB>(row, k + (lane >> 4)));
+          ldmatrix_x4(r, kd + R::at(row, k + (lane >> 4)));
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int kk = k + (i >> 1);
@@ -668,7 +671,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_attend(AttendArgs a) {
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
           uint32_t r[4];
-          ldmatrix_x4(r, kd + swz<RB>(row, 2 * k + ((lane >> 3) & 1)));
+          ldmatrix_x4(r, kd + R::at(row, 2 * k + ((lane >> 3) & 1)));
           const uint32_t qf[4] = {qa[k][0], RH == 2 ? qa[k][RH - 1] : 0u, qa[k][RH],
                                   RH == 2 ? qa[k][2 * RH - 1] : 0u};
           mma16816<MT>(s[2 * t], qf, r[0], r[1]);
@@ -698,19 +701,19 @@ __global__ void __launch_bounds__(kWarps * 32) k_attend(AttendArgs a) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) s[i][2 * r + j] *= k;
       }
-      if (mask != (TOK == 32 ? ~0u : 0xffffu)) {
+      if (mask != ALL) {
 #pragma unroll
         for (int i = 0; i < TT; ++i)
 #pragma unroll
           for (int j = 0; j < 2; ++j)
-            if (!((mask >> (i * 8 + c4 * 2 + j)) & 1)) s[i][2 * r + j] = __int_as_float(0xff800000);
+            if (!((mask >> (i * 8 + c4 * 2 + j)) & 1)) s[i][2 * r + j] = NEG_INF;
       }
       float top = m[r];
 #pragma unroll
       for (int i = 0; i < TT; ++i) top = fmaxf(top, fmaxf(s[i][2 * r], s[i][2 * r + 1]));
       top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
       top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-      const float z = top == __int_as_float(0xff800000) ? 0.f : top;
+      const float z = zero_if_empty(top);
       al[r] = exp2_approx(m[r] - z);
       grew |= top != m[r];
       m[r] = top;
@@ -755,7 +758,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_attend(AttendArgs a) {
 #pragma unroll
       for (int k = 0; k < CPR; k += 2) {
         uint32_t r[4];
-        ldmatrix_x4_trans(r, vd + swz<RB>(row, k + (lane >> 4)));
+        ldmatrix_x4_trans(r, vd + R::at(row, k + (lane >> 4)));
         if constexpr (KV == MOE_DT_E4M3) {
           // a 16-bit element holds values 2n, 2n + 1 of a token; a register two
           // tokens' pairs.  Bytes 0, 2 (values 2n) feed one tile, 1, 3 the next.
@@ -781,9 +784,12 @@ __global__ void __launch_bounds__(kWarps * 32) k_attend(AttendArgs a) {
       }
     }
 
-    stage = stage + 1 == S ? 0 : stage + 1;
-    const bool done = cc.tile + 1 == cc.nt;
-    if (done || u + 1 == u1) {
+    if (!R::EARLY) {  // the stage is free: the tile S ahead goes there
+      __syncwarp();
+      issue_next(stage);
+    }
+    if (++stage == S) stage = 0;
+    if (cc.tile + 1 == cc.nt || u + 1 == u1) {
       end_item(u - cc.tile, t0, cc.tile + 1, u + 1 == u1);
       if (u + 1 < u1) {
         cc.next(a, nh);
@@ -802,8 +808,9 @@ __global__ void __launch_bounds__(kWarps * 32) k_attend(AttendArgs a) {
 int rows_of(int G, int D) { return G <= 8 || D > 128 ? 8 : 16; }
 
 template <int KV, int DP, int RH>
-moe_status launch_attend(const AttendArgs& a, cudaStream_t s) {
-  constexpr int smem = Ring<KV, DP>::BYTES + (RH == 1 ? 2 : 1) * 8 * RH * DP * 4;
+moe_status launch_attend(AttendArgs a, cudaStream_t s) {
+  using R = Ring<KV, DP, RH>;
+  constexpr int smem = R::BYTES + (RH == 1 ? 2 : 1) * 8 * RH * DP * 4;
   static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is raised
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return launch_status(cudaErrorUnknown);
@@ -814,11 +821,11 @@ moe_status launch_attend(const AttendArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return launch_status(e);
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
-  // no more CTAs than tiles there can be
-  constexpr int TILE = Ring<KV, DP>::TILE;
-  const int64_t tiles = ((int64_t)a.max_pages * a.c.page_size + TILE - 1) / TILE;
-  const double most = (double)a.B * a.c.Hkv * a.nhb * (double)(tiles > 0 ? tiles : 1);
-  const int resident = smem > 113 * 1024 ? kSMs : kMaxCtas;
+  // tiles there can be: counted in 32 bits on the device
+  const int64_t tiles = ((int64_t)a.cap + R::TILE - 1) / R::TILE + 1;
+  const double most = (double)a.B * a.c.Hkv * a.nhb * (double)tiles;
+  if (most >= 2147483648.0) return MOE_ERR_UNSUPPORTED;
+  const int resident = R::CTAS * kSMs;
   const int grid = most < resident ? (int)most : resident;
   return launch_status(launch_pdl(k_attend<KV, DP, RH>, grid, kWarps * 32, smem, s, a));
 }
@@ -827,7 +834,7 @@ template <int KV>
 moe_status pick_attend(const AttendArgs& a, cudaStream_t s) {
   const int D = a.c.D;
   if (D > 128) return launch_attend<KV, 256, 1>(a, s);
-  if (rows_of(a.G, D) == 8)
+  if (rows_of(a.G, a.c.D) == 8)
     return D <= 64 ? launch_attend<KV, 64, 1>(a, s) : launch_attend<KV, 128, 1>(a, s);
   return D <= 64 ? launch_attend<KV, 64, 2>(a, s) : launch_attend<KV, 128, 2>(a, s);
 }
@@ -921,7 +928,9 @@ MOE_API moe_status kvcache_attend(const kvcache_attend_args* a, void* stream) {
   k.q = a->q, k.out = a->out, k.lse = a->lse;
   k.q_row = a->q_row, k.q_head = a->q_head, k.out_row = a->out_row, k.out_head = a->out_head;
   k.table_ld = a->table_ld, k.page_table = a->page_table, k.seq_lens = a->seq_lens;
-  k.max_pages = a->max_pages, k.window = a->window, k.q_bf16 = a->dtype == MOE_DT_BF16;
+  const int64_t cap = (int64_t)a->max_pages * a->c.page_size;
+  k.cap = cap > 0x7ffffe00 ? 0x7ffffe00 : (int)cap;  // positions, and tiles' ends, within int
+  k.window = a->window, k.q_bf16 = a->dtype == MOE_DT_BF16;
   k.scale = a->scale, k.softcap = a->softcap;
   // for pos < 2^31: floor(pos / d) = pos * ceil(2^(31 + s) / d) >> (31 + s), 2^s >= d
   k.div_shift = 31;

@@ -1,0 +1,463 @@
+// w4_body.cuh - K-w4: linear products of a few tokens with 4-bit weights that carry
+// a scale (and zero point) per group of input values (moe_w4_linear).
+//
+// y[t][n] = sum_G s[n][G] * sum_{k in G} (value(code) - zero) x[t][k] + bias[n]
+//
+// Bound by reading the codes once: half a byte a weight, so the instructions per
+// weight decide.  A warp takes 16 rows of W and every n-th chunk of 256 input
+// values; it streams its codes through its own ring of cp.async stages.  ldmatrix
+// on the raw codes hands a thread 8 consecutive codes of a row, four threads 32:
+// that is one scale group of 32 or a part of a larger one, so every group size
+// sums inside the matrix instructions in fp32 and the scale multiplies once a
+// group.
+// The warps that share a chunk (WR of them, for different rows) share its x in
+// shared memory.  The K split of a CTA (WK) and of a cluster is added up in a
+// fixed order at the end, the cluster's through distributed shared memory.
+#pragma once
+
+#include <atomic>
+
+#include "elem.cuh"
+#include "sm100_ptx.cuh"
+
+namespace moe {
+
+struct W4Args {
+  int T, N, K, G, g32, zrow;           // G groups of 32 * g32 values; zero bytes a row
+  int wk;                              // warps along K in a CTA
+  const uint16_t* x;
+  const uint8_t* codes;
+  const uint16_t* scales;
+  const uint8_t* zeros;
+  const uint16_t* bias;
+  uint16_t* y;
+  int64_t ldx, ldy;
+};
+
+namespace {
+
+constexpr int kChunk = 256;            // input values of a stage: 128 bytes of a row
+constexpr int kTokens = 16;            // tokens of one pass over the weights
+constexpr int kXPitch = kChunk * 2 + 64;  // bytes of a token's chunk: two tokens' reads meet
+                                          // in different halves of the banks
+
+// Codes reach the matrix instructions as exact f16 numbers, by as few instructions
+// as there are: E2M1 by the conversion instruction; u4 by masks alone, a nibble
+// reading as the subnormal n 2^-24 (and the second nibble of a byte, where it
+// stands, as 16 n 2^-24).  What that asks of x is done once a chunk and token, in
+// shared memory (`prepare_x`), not once a row:
+//   - bf16 goes to f16 under a power of two that brings the chunk's largest value to
+//     [2^14, 2^15): exact but for values 2^-29 below it;
+//   - for u4, the pairs that meet second nibbles are divided by 16 (so f16 is scaled
+//     likewise, and keeps its digits), x is laid in the order of the nibbles, and
+//     its sums over each group are kept, with which the zero points come off:
+//     sum (n - zero) x = sum n x - zero sum x.
+// Subtracting zero points from every code instead, with packed 16-bit arithmetic,
+// took 9.3 us against REPLACE at 1 x 6144 x 6144.
+template <int DT, int FMT>
+constexpr bool kPrepares = DT == MOE_DT_BF16 || FMT == MOE_W4_U4;
+
+// 8 codes (nibble i = value i) -> pairs (0, 4), (1, 5), (2, 6), (3, 7) for u4,
+// (0, 1), (2, 3), ... for E2M1
+template <int FMT>
+__device__ __forceinline__ void expand(uint32_t v, uint32_t (&o)[4]) {
+  if constexpr (FMT == MOE_W4_E2M1) {
+    e2m1x8_to_f16x2x4(v, o);
+  } else {
+    const uint32_t u = v >> 8;
+    o[0] = v & 0x000f000fu;
+    o[1] = v & 0x00f000f0u;
+    o[2] = u & 0x000f000fu;
+    o[3] = u & 0x00f000f0u;
+  }
+}
+// A warp's chunk of one token, 8 values a lane; sum: of the lane's scaled values.
+// Returns what undoes the power of two.
+template <int DT, int FMT>
+__device__ __forceinline__ float prepare_x(uint4& v, float& sum) {
+  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+  uint32_t m = __vmaxu2(__vmaxu2(u[0] & 0x7fff7fffu, u[1] & 0x7fff7fffu),
+                        __vmaxu2(u[2] & 0x7fff7fffu, u[3] & 0x7fff7fffu));
+  m = __reduce_max_sync(~0u, max(m & 0xffffu, m >> 16));
+  // exponent of the largest value; infinities and NaN keep their meaning under any
+  // power, and the largest finite values beside them come down to f16 as well
+  const int e = DT == MOE_DT_BF16 ? min((int)(m >> 7), 254) - 127
+                                  : (int)(__float_as_uint(f16_to_f32((uint16_t)min(m, 0x7bffu))) >> 23) - 127;
+  const int up = m == 0 ? 0 : min(14 - e, 100);
+  const float f = __uint_as_float((uint32_t)(127 + up) << 23);
+  float x[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[2 * i] = lo2<DT>(u[i]) * f, x[2 * i + 1] = hi2<DT>(u[i]) * f;
+  if constexpr (FMT == MOE_W4_U4) {
+    sum = ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+    v = make_uint4(pack_f16(x[0], x[4]), pack_f16(x[1] * 0.0625f, x[5] * 0.0625f),
+                   pack_f16(x[2], x[6]), pack_f16(x[3] * 0.0625f, x[7] * 0.0625f));
+  } else {
+    v = make_uint4(pack_f16(x[0], x[1]), pack_f16(x[2], x[3]), pack_f16(x[4], x[5]),
+                   pack_f16(x[6], x[7]));
+  }
+  return __uint_as_float((uint32_t)(127 - up) << 23);
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+// fp32 at the address of this CTA's shared memory, read from CTA `rank` of the cluster
+__device__ __forceinline__ float cluster_load(uint32_t addr, uint32_t rank) {
+  float v;
+  asm volatile("{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %1, %2;\n"
+               " ld.shared::cluster.f32 %0, [a];\n}"
+               : "=f"(v)
+               : "r"(addr), "r"(rank)
+               : "memory");
+  return v;
+}
+
+template <int WR>
+struct Stages {
+  static constexpr int S = WR == 1 ? 3 : 2;
+};
+
+// NT: token tiles of 8.  WR: warps along the rows of W,
+// which share x.  G32: the group's length in blocks of 32 values where it is 1, 2 or 4,
+// so that its ends are known at compile time and its scales come a chunk ahead; 0: any.
+template <int DT, int FMT, int NT, int WR, int G32>
+__global__ void __launch_bounds__(256) k_w4(W4Args a) {
+  constexpr bool PREP = kPrepares<DT, FMT>, U4 = FMT == MOE_W4_U4;
+  constexpr int S = Stages<WR>::S;          // all under way; a stage is refilled once used
+  constexpr int ROWS = 16;                  // of a warp
+  constexpr int STAGE = ROWS * kChunk / 2;  // bytes of one warp's stage of codes
+  constexpr int NG = G32 ? 8 / G32 : 1;     // groups of a chunk
+  constexpr int SV = NG == 8 ? 2 : 1;       // of which a lane fetches this many
+  extern __shared__ __align__(128) uint8_t sm[];
+  __shared__ float undo[8 / WR][NT * 8];    // of each chunk in work: what undoes x's power
+  __shared__ float xsum[8 / WR][NT * 8][8]; // u4: sums of x over its groups (G32 0: blocks)
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int wr = w % WR, kw = w / WR;       // place along rows, along K
+  const int g = lane >> 2, c4 = lane & 3;
+  const int crank = cluster_rank(), csize = cluster_size();
+  const int n0 = ((blockIdx.x / csize) * WR + wr) * ROWS, t0 = blockIdx.y * kTokens;
+  const int nt = min(a.T - t0, NT * 8);     // tokens of this CTA
+  const int chunks = (a.K + kChunk - 1) / kChunk;
+  const int step = a.wk * csize;            // this warp: chunks first, first + step, ...
+  const int first = crank * a.wk + kw;
+  const int64_t krow = a.K / 2;
+  const int xstage = nt * kXPitch;
+  const uint32_t cring = ptx::smem_u32(sm) + w * S * STAGE;
+  uint8_t* xbase = sm + a.wk * WR * S * STAGE + kw * S * xstage;
+  pdl_wait();
+  pdl_launch_dependents();
+
+  // Rows past the last read the last row again: their results go nowhere.  The
+  // same for tokens past the last.  Past K there are zeros.
+  const int r0 = lane >> 3;
+  const uint8_t* csrc[ROWS / 4];
+#pragma unroll
+  for (int i = 0; i < ROWS / 4; ++i)
+    csrc[i] = a.codes + (int64_t)min(n0 + i * 4 + r0, a.N - 1) * krow + (lane & 7) * 16;
+  const uint32_t cdst0 = cring + r0 * 128 + ((lane & 7) ^ r0) * 16;        // rows r0, r0 + 8, ...
+  const uint32_t cdst1 = cring + r0 * 128 + ((lane & 7) ^ (r0 + 4)) * 16;  // r0 + 4, r0 + 12, ...
+  const uint16_t* xsrc = a.x + (t0 + min(wr, nt - 1)) * a.ldx + lane * 8;
+  const uint32_t xdst = ptx::smem_u32(xbase) + wr * kXPitch + lane * 16;
+  auto issue = [&](int kc, int stage) {
+    if (kc < chunks) {
+      const int64_t at = (int64_t)kc * (kChunk / 2);
+      const bool in = at + (lane & 7) * 16 < krow;
+#pragma unroll
+      for (int i = 0; i < ROWS / 4; ++i)
+        cp_async16((i & 1 ? cdst1 : cdst0) + stage * STAGE + i * 512, in ? csrc[i] + at : a.codes,
+                   in ? 16 : 0);
+      const bool xin = kc * kChunk + lane * 8 < a.K;
+      const uint16_t* xs = xin ? xsrc + (int64_t)kc * kChunk : a.x;
+      uint32_t xd = xdst + stage * xstage;
+#pragma unroll 1
+      for (int t = wr; t < nt; t += WR, xs += xin ? WR * a.ldx : 0, xd += WR * kXPitch)
+        cp_async16(xd, xs, xin ? 16 : 0);
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < S; ++i) issue(first + i * step, i);
+
+  // Scale (high half) and zero point of the warp's rows h * 8 + g and a group: with
+  // G32 the four lanes of a row fetch one group each of the next chunk (two each
+  // of eight), ahead of its work
+  const uint16_t* sp[2];
+  const uint8_t* zp[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int64_t row = min(n0 + h * 8 + g, a.N - 1);
+    sp[h] = a.scales + row * a.G + (G32 ? c4 % NG : 0);
+    zp[h] = a.zeros ? a.zeros + row * a.zrow + (G32 ? c4 % NG / 2 : 0) : nullptr;
+  }
+  uint32_t cur[2][SV] = {}, nxt[2][SV] = {};
+  auto fetch_scales = [&](int kc) {
+    if constexpr (G32 != 0) {
+#pragma unroll
+      for (int v = 0; v < SV; ++v) {
+        if (kc * NG + v * 4 + c4 % NG >= a.G) continue;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          nxt[h][v] = (uint32_t)sp[h][kc * NG + v * 4] << 16;
+          if constexpr (FMT == MOE_W4_U4)
+            nxt[h][v] |= zp[h] ? (zp[h][kc * (NG / 2) + v * 2] >> (4 * (c4 & 1))) & 15 : 8;
+        }
+      }
+    }
+  };
+  auto scale_word = [&](int h, int grp) {  // G32 == 0: at its beginning
+    uint32_t v = (uint32_t)sp[h][grp] << 16;
+    if constexpr (FMT == MOE_W4_U4) v |= zp[h] ? (zp[h][grp / 2] >> (4 * (grp & 1))) & 15 : 8;
+    return v;
+  };
+  fetch_scales(first);
+
+  float acc[NT][4] = {}, sum[NT][4];
+  int stage = 0;
+  auto group_sync = [&]() {  // the warps that share a chunk
+    if constexpr (WR == 1) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(1 + kw), "n"(WR * 32) : "memory");
+  };
+  const uint32_t crow = cring + (lane & 15) * 128;
+  const uint8_t* xrow[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) xrow[n] = xbase + min(n * 8 + g, nt - 1) * kXPitch + c4 * 16;
+#pragma unroll 1
+  for (int kc = first; kc < chunks; kc += step) {
+    cp_async_wait<S - 1>();
+    group_sync();
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int v = 0; v < SV; ++v) cur[h][v] = nxt[h][v];
+    fetch_scales(kc + step);
+    const uint32_t cb = crow + stage * STAGE;
+    const int blocks = min(8, a.K / 32 - kc * 8);  // of 32 values, in this chunk
+    float back[NT][2];
+    if constexpr (PREP) {
+#pragma unroll 1
+      for (int t = wr; t < nt; t += WR) {
+        uint4* p = (uint4*)(xbase + stage * xstage + t * kXPitch + lane * 16);
+        uint4 v = *p;
+        float sx;
+        const float u = prepare_x<DT, FMT>(v, sx);
+        *p = v;
+        if constexpr (U4) {
+          constexpr int BLOCKS = G32 ? G32 : 1;  // lanes 4 i .. 4 i + 3 hold block i
+#pragma unroll
+          for (int o = 1; o < 4 * BLOCKS; o *= 2) sx += __shfl_xor_sync(~0u, sx, o);
+          if (lane % (4 * BLOCKS) == 0) xsum[kw][t][lane / (4 * BLOCKS)] = sx;
+        }
+        if (lane == 0) undo[kw][t] = u;
+      }
+      group_sync();
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) back[n][q] = undo[kw][min(n * 8 + c4 * 2 + q, nt - 1)];
+    }
+    // G32 == 0: the scale group, and what is left of it in blocks
+    int grp = G32 ? 0 : kc * 8 / a.g32;
+    int left = G32 ? 0 : (grp + 1) * a.g32 - kc * 8;
+    uint32_t s[2];
+    float sx[NT][2];
+    auto begin_group = [&](int local) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if constexpr (G32 == 0) s[h] = scale_word(h, grp);
+        else s[h] = __shfl_sync(~0u, cur[h][local / 4 % SV], (lane & 28) | (local & 3));
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) sum[n][q] = 0.f;
+        sx[n][0] = sx[n][1] = 0.f;
+      }
+    };
+    // 32 input values
+    auto block = [&](uint32_t c0, uint32_t c1, const uint4 (&xv)[NT], int j, bool last) {
+      uint32_t p[2][4];
+      expand<FMT>(c0, p[0]);
+      expand<FMT>(c1, p[1]);
+      const uint32_t lo[4] = {p[0][0], p[1][0], p[0][1], p[1][1]};
+      const uint32_t hi[4] = {p[0][2], p[1][2], p[0][3], p[1][3]};
+#pragma unroll
+      for (int n = 0; n < NT; ++n) mma16816<MOE_DT_F16>(sum[n], lo, xv[n].x, xv[n].y);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) mma16816<MOE_DT_F16>(sum[n], hi, xv[n].z, xv[n].w);
+      // the group ends here, or this warp's part of it does
+      const bool end = G32 ? (j + 1) % (G32 ? G32 : 1) == 0 : --left == 0 || last;
+      if constexpr (U4) {
+        if (G32 == 0 || end) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+              sx[n][q] += xsum[kw][min(n * 8 + c4 * 2 + q, nt - 1)][G32 ? j / (G32 ? G32 : 1) : j];
+        }
+      }
+      if (end) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          // u4 sums are in units of 2^-24
+          const float f = to_f32<DT>((uint16_t)(s[h] >> 16)) * (U4 ? 16777216.f : 1.f);
+          const float zero = U4 ? (float)(s[h] & 0xffu) * 5.9604644775390625e-8f : 0.f;
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              float v = sum[n][2 * h + q];
+              if constexpr (U4) v -= zero * sx[n][q];
+              acc[n][2 * h + q] += f * (PREP ? v * back[n][q] : v);
+            }
+        }
+        if (!last) {
+          if (!G32) ++grp, left = a.g32;
+          begin_group(G32 ? (j + 1) / (G32 ? G32 : 1) : 0);
+        }
+      }
+    };
+    begin_group(0);
+    const uint8_t* xs[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) xs[n] = xrow[n] + stage * xstage;
+    if (blocks == 8) {
+      // a quarter of a chunk's codes, and its x, in registers before its products begin
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) {
+        uint32_t c[4];
+        ldmatrix_x4(c, cb + ((j + (lane >> 4)) ^ (lane & 7)) * 16);
+        uint4 xv[2][NT];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) xv[k][n] = *(const uint4*)(xs[n] + (j + k) * 64);
+        block(c[0], c[1], xv[0], j, false);
+        block(c[2], c[3], xv[1], j + 1, j + 1 == 7);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 7; ++j)
+        if (j < blocks) {
+          uint32_t c[2];
+          uint4 xv[NT];
+          ldmatrix_x2(c, cb + (j ^ (lane & 7)) * 16);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) xv[n] = *(const uint4*)(xs[n] + j * 64);
+          block(c[0], c[1], xv, j, j + 1 == blocks);
+        }
+    }
+    group_sync();
+    issue(kc + S * step, stage);
+    stage = stage + 1 == S ? 0 : stage + 1;
+  }
+  cp_async_wait<0>();
+  __syncthreads();
+
+  // sums over the warps along K in their order, then over the cluster in rank
+  // order; the outputs are dealt to its CTAs
+  constexpr int OUT = WR * NT * 128;
+  float* red = (float*)sm;
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) red[(w * NT + n) * 128 + q * 32 + lane] = acc[n][q];
+  __syncthreads();
+  if (csize > 1) {
+#pragma unroll 1
+    for (int i = threadIdx.x; i < OUT; i += blockDim.x) {
+      float v = red[i];
+      for (int k = 1; k < a.wk; ++k) v += red[k * OUT + i];
+      red[i] = v;
+    }
+    cluster_sync();
+  }
+  const uint32_t red_addr = ptx::smem_u32(red);
+#pragma unroll 1
+  for (int i = threadIdx.x + crank * blockDim.x; i < OUT; i += blockDim.x * csize) {
+    const int ln = i & 31, q = (i >> 5) & 3, n = (i >> 7) % NT, m = (i >> 7) / NT;
+    const int row = (blockIdx.x / csize) * (ROWS * WR) + m * 16 + (q >> 1) * 8 + (ln >> 2);
+    const int t = n * 8 + (ln & 3) * 2 + (q & 1);
+    if (row < a.N && t < nt) {
+      float v = 0.f;
+      if (csize > 1) {
+        for (int k = 0; k < csize; ++k) v += cluster_load(red_addr + i * 4, k);
+      } else {
+        for (int k = 0; k < a.wk; ++k) v += red[k * OUT + i];
+      }
+      if (a.bias) v += to_f32<DT>(a.bias[row]);
+      a.y[(t0 + t) * a.ldy + row] = from_f32<DT>(v);
+    }
+  }
+  if (csize > 1) cluster_sync();  // until all have read
+}
+
+template <int DT, int FMT, int NT, int WR, int G32>
+moe_status launch_w4(W4Args a, cudaStream_t s) {
+  auto* kern = k_w4<DT, FMT, NT, WR, G32>;
+  static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is raised
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return launch_status(cudaErrorUnknown);
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(ready.load(std::memory_order_relaxed) & bit)) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+    if (e != cudaSuccess) return launch_status(e);
+    ready.fetch_or(bit, std::memory_order_relaxed);
+  }
+  constexpr int ROWS = 16 * WR;
+  const int chunks = (a.K + kChunk - 1) / kChunk;
+  const int tiles = (a.N + ROWS - 1) / ROWS, passes = (a.T + kTokens - 1) / kTokens;
+  const int nt = a.T < NT * 8 ? a.T : NT * 8;
+  // 8 warps a CTA, then a cluster along K while the GPU would have fewer than
+  // `FEW` CTAs and a warp keeps a chunk
+  a.wk = 8 / WR < chunks ? 8 / WR : chunks;
+  constexpr int FEW = WR == 1 ? kSMs : kSMs * 4 / 3;
+  int cluster = 1;
+  while (cluster < 8 && (int64_t)tiles * passes * cluster <= FEW && a.wk * cluster * 2 <= chunks)
+    cluster *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(tiles * cluster, passes);
+  cfg.blockDim = dim3(a.wk * WR * 32);
+  cfg.dynamicSmemBytes = (size_t)a.wk * Stages<WR>::S * (ROWS * (kChunk / 2) + nt * kXPitch);
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return launch_status(cudaLaunchKernelEx(&cfg, kern, a));
+}
+
+template <int DT, int FMT, int NT, int WR>
+moe_status pick_group(const W4Args& a, cudaStream_t s) {
+  if (a.g32 == 1) return launch_w4<DT, FMT, NT, WR, 1>(a, s);
+  if (a.g32 == 2) return launch_w4<DT, FMT, NT, WR, 2>(a, s);
+  if (a.g32 == 4) return launch_w4<DT, FMT, NT, WR, 4>(a, s);
+  return launch_w4<DT, FMT, NT, WR, 0>(a, s);
+}
+
+// One token: each warp keeps its own x (no barrier between warps).  More are
+// prepared once for 8 warps of different rows.
+template <int DT, int FMT>
+moe_status pick_w4(const W4Args& a, cudaStream_t s) {
+  if (a.T == 1) return pick_group<DT, FMT, 1, 1>(a, s);
+  return a.T <= 8 ? pick_group<DT, FMT, 1, 8>(a, s) : pick_group<DT, FMT, 2, 8>(a, s);
+}
+
+}  // namespace
+}  // namespace moe
