@@ -1,10 +1,14 @@
 """Builds libmoe.so (all CUDA sources, sm_103a) in-tree with nvcc, one
-translation unit per process, then links.  No CMake."""
+translation unit per process, then links; and _block.so, the decode-block calls
+on torch tensors (g++ against torch's headers).  No CMake."""
 from __future__ import annotations
 
+import importlib.util
 import os
+import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -14,14 +18,29 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe.so")
 SOURCES = ["route.cu", "route_tc.cu", "permute.cu", "cache.cu", "decode.cu", "prefill.cu", "api.cu",
            "noalloc.cu", "block_norm.cu", "kvcache.cu", "w4.cu", "w4_f16.cu"]
+BLOCK = os.path.join(HERE, "_block.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hidden",
          "-I" + INCLUDE, "-I" + CSRC]
 
 
+def _block_command() -> list:
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(shutil.which("nvcc"))))
+    lib = os.path.join(torch, "lib")
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+            "-I" + INCLUDE, "-I" + sysconfig.get_paths()["include"],
+            "-isystem", os.path.join(torch, "include"),
+            "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+            "-isystem", os.path.join(cuda, "include"),
+            os.path.join(CSRC, "torch_block.cpp"), "-o", BLOCK, "-L" + lib, "-Wl,-rpath," + lib,
+            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+
+
 def build(verbose: bool = False, ptxas_verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    objs, procs = [], []
+    cmd = _block_command()
+    objs, procs = [], [(cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT))]
     for src in SOURCES:
         obj = os.path.join(BUILD, src.replace(".cu", ".o"))
         cmd = ["nvcc", *ARCH, *FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
@@ -34,7 +53,7 @@ def build(verbose: bool = False, ptxas_verbose: bool = False) -> str:
         out, _ = p.communicate()
         logs.append(out.decode())
         if p.returncode != 0:
-            raise RuntimeError(f"nvcc failed: {' '.join(cmd)}\n{out.decode()}")
+            raise RuntimeError(f"failed: {' '.join(cmd)}\n{out.decode()}")
     link = ["nvcc", *ARCH, "-shared", "-o", LIB, *objs]
     p = subprocess.run(link, capture_output=True, text=True)
     if p.returncode != 0:

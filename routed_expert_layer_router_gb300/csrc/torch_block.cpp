@@ -1,0 +1,437 @@
+// torch_block.cpp - the CPython module `_block`: the decode-block calls of
+// include/moe.h on torch tensors.  It checks shapes, types and strides, makes
+// the outputs a caller did not give, fills the call's structure and calls the
+// library on the current stream; block.py holds the documented functions and
+// classes over it.  (The same in Python over ctypes costs 12 us a call on a
+// Grace core against REPLACE here, and several of the kernels take 2.)
+//
+// The library's functions and its Python exception come in through bind().
+#define PY_SSIZE_T_CLEAN
+#include <Python.h>
+
+#include <ATen/core/Tensor.h>
+#include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAGuard.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include "moe.h"
+
+namespace {
+
+using at::Tensor;
+
+moe_status (*f_norm)(const moe_block_norm_args*, void*);
+moe_status (*f_append)(const kvcache_append_args*, void*);
+moe_status (*f_attend)(const kvcache_attend_args*, void*);
+moe_status (*f_w4)(const moe_w4_linear_args*, void*);
+PyObject* moe_error;  // MoeError(call, status)
+
+#define WANT(ok, ...)                          \
+  do {                                         \
+    if (!(ok)) {                               \
+      PyErr_Format(PyExc_ValueError, __VA_ARGS__); \
+      return nullptr;                          \
+    }                                          \
+  } while (0)
+#define TRY(expr)                \
+  do {                           \
+    if (!(expr)) return nullptr; \
+  } while (0)
+
+int type_code(at::ScalarType t) {
+  switch (t) {
+    case at::kBFloat16: return MOE_DT_BF16;
+    case at::kFloat: return MOE_DT_F32;
+    case at::kHalf: return MOE_DT_F16;
+    case at::kFloat8_e4m3fn: return MOE_DT_E4M3;
+    default: return -1;
+  }
+}
+at::ScalarType type_of(long code) {
+  return code == MOE_DT_BF16 ? at::kBFloat16 : code == MOE_DT_F16 ? at::kHalf : at::kFloat;
+}
+
+// a tensor argument; None leaves *out null
+bool take(PyObject* o, const char* name, const Tensor** out) {
+  *out = nullptr;
+  if (o == Py_None) return true;
+  if (!THPVariable_Check(o)) {
+    PyErr_Format(PyExc_TypeError, "%s: a tensor is wanted", name);
+    return false;
+  }
+  *out = &THPVariable_Unpack(o);
+  return true;
+}
+bool take_needed(PyObject* o, const char* name, const Tensor** out) {
+  if (!take(o, name, out)) return false;
+  if (*out) return true;
+  PyErr_Format(PyExc_TypeError, "%s: a tensor is wanted", name);
+  return false;
+}
+bool real(PyObject* o, float* out) {
+  const double v = PyFloat_AsDouble(o);
+  *out = (float)v;
+  return !(v == -1.0 && PyErr_Occurred());
+}
+bool whole(PyObject* o, int* out) {
+  const long v = PyLong_AsLong(o);
+  if (v == -1 && PyErr_Occurred()) return false;
+  if (v != (int)v) {
+    PyErr_SetString(PyExc_ValueError, "an integer of 32 bits is wanted");
+    return false;
+  }
+  *out = (int)v;
+  return true;
+}
+
+// t as T contiguous rows of H values: their stride
+bool rows(const Tensor& t, int64_t T, int64_t H, const char* name, int64_t* ld) {
+  if (!t.is_cuda() || t.dim() != 2 || t.size(0) != T || t.size(1) != H ||
+      (H != 1 && t.stride(1) != 1)) {
+    PyErr_Format(PyExc_ValueError, "%s: [%lld, %lld] on the GPU with contiguous rows is wanted",
+                 name, (long long)T, (long long)H);
+    return false;
+  }
+  const int64_t row = t.stride(0);
+  *ld = T > 1 || row >= H ? row : H;
+  return true;
+}
+// row and head strides of t, [N, heads, D]
+bool heads(const Tensor& t, int64_t N, int64_t D, const char* name, int64_t* row, int64_t* head) {
+  if (!t.is_cuda() || t.dim() != 3 || t.size(0) != N || t.size(2) != D || t.stride(2) != 1) {
+    PyErr_Format(PyExc_ValueError, "%s: [%lld, heads, %lld] on the GPU is wanted", name,
+                 (long long)N, (long long)D);
+    return false;
+  }
+  *row = t.stride(0);
+  *head = t.stride(1);
+  return true;
+}
+bool ints(const Tensor& t, int64_t dims, const char* name) {
+  if (!t.is_cuda() || t.scalar_type() != at::kInt || t.dim() != dims ||
+      (t.numel() > 1 && t.size(-1) > 1 && t.stride(-1) != 1)) {
+    PyErr_Format(PyExc_ValueError, "%s: int32 with %lld dimensions and contiguous rows on the GPU "
+                 "is wanted", name, (long long)dims);
+    return false;
+  }
+  return true;
+}
+// a weight vector; all given ones share a type
+bool vector(const Tensor* t, int64_t n, const char* name, int* type, const void** p) {
+  *p = nullptr;
+  if (!t) return true;
+  const int code = type_code(t->scalar_type());
+  if (!t->is_cuda() || t->dim() != 1 || t->size(0) != n || !t->is_contiguous() || code < 0 ||
+      (*type >= 0 && code != *type)) {
+    PyErr_Format(PyExc_ValueError, "%s: a contiguous [%lld] of the other weights' type on the GPU "
+                 "is wanted", name, (long long)n);
+    return false;
+  }
+  *type = code;
+  *p = t->const_data_ptr();
+  return true;
+}
+bool fits(int64_t v, const char* name) {
+  if (v <= 0x7fffffff) return true;
+  PyErr_Format(PyExc_ValueError, "%s: too large", name);
+  return false;
+}
+
+PyObject* fail(const char* call, moe_status st) {
+  PyObject* args = Py_BuildValue("(si)", call, (int)st);
+  if (args) PyErr_SetObject(moe_error, args);
+  Py_XDECREF(args);
+  return nullptr;
+}
+PyObject* wrap(const Tensor& made, PyObject* given) {
+  if (given != Py_None) {
+    Py_INCREF(given);
+    return given;
+  }
+  if (made.defined()) return THPVariable_Wrap(made);
+  Py_RETURN_NONE;
+}
+PyObject* pair(PyObject* a, PyObject* b) {
+  PyObject* t = a && b ? PyTuple_Pack(2, a, b) : nullptr;
+  Py_XDECREF(a);
+  Py_XDECREF(b);
+  return t;
+}
+// the device of `t`, current for the call, and its current stream
+struct Place {
+  c10::cuda::CUDAGuard guard;
+  void* stream;
+  explicit Place(const Tensor& t)
+      : guard(t.device()), stream(c10::cuda::getCurrentCUDAStream(t.device().index()).stream()) {}
+};
+
+// block_norm(x, y, w_pre, w_post, b_pre, b_post, post_norm, gate, gate_sigmoid,
+//            res_scale, branch_scale, eps, kind, w_offset, r, h, need_r, need_h, h_type)
+PyObject* block_norm(PyObject*, PyObject* const* o, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  WANT(n == 19, "19 arguments are wanted");
+  const Tensor *x, *y, *w_pre, *w_post, *b_pre, *b_post, *gate, *r, *h;
+  TRY(take_needed(o[0], "x", &x) && take(o[1], "y", &y) && take(o[2], "w_pre", &w_pre) &&
+      take(o[3], "w_post", &w_post) && take(o[4], "b_pre", &b_pre) &&
+      take(o[5], "b_post", &b_post) && take(o[7], "gate", &gate) && take(o[14], "r", &r) &&
+      take(o[15], "h", &h));
+  WANT(x->is_cuda() && x->dim() == 2, "x: [T, H] on the GPU is wanted");
+  const int64_t T = x->size(0), H = x->size(1);
+  moe_block_norm_args a = {};
+  TRY(fits(T, "T") && fits(H, "H"));
+  a.T = (int)T;
+  a.H = (int)H;
+  TRY(rows(*x, T, H, "x", &a.ldx));
+  a.x = x->const_data_ptr();
+  a.stream_type = type_code(x->scalar_type());
+  at::ScalarType branch = x->scalar_type();
+  if (y) {
+    TRY(rows(*y, T, H, "y", &a.ldy));
+    a.y = y->const_data_ptr();
+    branch = y->scalar_type();
+  }
+  int code;
+  TRY(whole(o[18], &code));
+  if (h) {
+    WANT(!y || h->scalar_type() == branch, "h: y's type is wanted");
+    branch = h->scalar_type();
+  } else if (!y && code >= 0) {
+    branch = type_of(code);
+  }
+  a.branch_type = type_code(branch);
+  int weight = -1;
+  TRY(vector(w_pre, H, "w_pre", &weight, &a.w_pre) &&
+      vector(w_post, H, "w_post", &weight, &a.w_post) &&
+      vector(b_pre, H, "b_pre", &weight, &a.b_pre) &&
+      vector(b_post, H, "b_post", &weight, &a.b_post));
+  a.weight_type = weight < 0 ? MOE_DT_F32 : weight;
+  a.post_norm = o[6] == Py_None ? (w_post || b_post) : PyObject_IsTrue(o[6]);
+  if (gate) {
+    const int64_t d = gate->dim(), last = d ? gate->size(d - 1) : 0;
+    WANT(gate->is_cuda() && gate->scalar_type() == branch &&
+             ((d == 1 && last == H) || (d == 2 && gate->size(0) == T && (last == H || last == 1))),
+         "gate: [H], [T, 1] or [T, H] of y's type on the GPU is wanted");
+    a.gate = gate->const_data_ptr();
+    a.gate_row = d == 2 ? gate->stride(0) : 0;
+    a.gate_col = last == H;
+    WANT(!a.gate_col || H == 1 || gate->stride(d - 1) == 1, "gate: contiguous rows are wanted");
+  }
+  a.gate_act = PyObject_IsTrue(o[8]) ? MOE_GATE_SIGMOID : MOE_GATE_NONE;
+  TRY(real(o[9], &a.res_scale) && real(o[10], &a.branch_scale) && real(o[11], &a.eps) &&
+      whole(o[12], &a.kind) && real(o[13], &a.w_offset));
+  Place at_(*x);
+  Tensor made_r, made_h;
+  a.ldr = a.ldh = H;
+  if (r) {
+    WANT(r->scalar_type() == x->scalar_type(), "r: x's type is wanted");
+    TRY(rows(*r, T, H, "r", &a.ldr));
+    a.r = r->mutable_data_ptr();
+  } else if (PyObject_IsTrue(o[16])) {
+    made_r = at::empty({T, H}, x->options());
+    a.r = made_r.mutable_data_ptr();
+  }
+  if (h) {
+    TRY(rows(*h, T, H, "h", &a.ldh));
+    a.h = h->mutable_data_ptr();
+  } else if (PyObject_IsTrue(o[17])) {
+    made_h = at::empty({T, H}, x->options().dtype(branch));
+    a.h = made_h.mutable_data_ptr();
+  }
+  const moe_status st = f_norm(&a, at_.stream);
+  if (st != MOE_OK) return fail("moe_block_norm", st);
+  return pair(wrap(made_r, o[14]), wrap(made_h, o[15]));
+  END_HANDLE_TH_ERRORS
+}
+
+// append(address of the handle's kvcache_append_args, k, v, page_table, pos, seq, q,
+//        cos, sin, interleaved, q_out)
+PyObject* append(PyObject*, PyObject* const* o, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  WANT(n == 11, "11 arguments are wanted");
+  const void* base = PyLong_AsVoidPtr(o[0]);
+  TRY(base);
+  kvcache_append_args a = *(const kvcache_append_args*)base;
+  const Tensor *k, *v, *table, *pos, *seq, *q, *cos, *sin, *out;
+  TRY(take_needed(o[1], "k", &k) && take_needed(o[2], "v", &v) &&
+      take_needed(o[3], "page_table", &table) && take_needed(o[4], "pos", &pos) &&
+      take(o[5], "seq", &seq) && take(o[6], "q", &q) && take(o[7], "cos", &cos) &&
+      take(o[8], "sin", &sin) && take(o[10], "q_out", &out));
+  TRY(ints(*pos, 1, "pos") && ints(*table, 2, "page_table"));
+  const int64_t N = pos->size(0), D = a.c.D;
+  TRY(fits(N, "N") && fits(table->size(0), "page_table") && fits(table->size(1), "page_table"));
+  TRY(heads(*k, N, D, "k", &a.k_row, &a.k_head) && heads(*v, N, D, "v", &a.v_row, &a.v_head));
+  WANT(k->size(1) == a.c.Hkv && v->size(1) == a.c.Hkv && k->scalar_type() == v->scalar_type(),
+       "k, v: %d heads of one type are wanted", a.c.Hkv);
+  a.N = (int)N;
+  a.dtype = type_code(k->scalar_type());
+  a.k = k->const_data_ptr();
+  a.v = v->const_data_ptr();
+  Place at_(*k);
+  Tensor made;
+  if (q) {
+    TRY(heads(*q, N, D, "q", &a.q_row, &a.q_head));
+    WANT(q->scalar_type() == k->scalar_type(), "q: the type of k is wanted");
+    TRY(fits(q->size(1), "q"));
+    a.Hq = (int)q->size(1);
+    a.q = q->const_data_ptr();
+    if (out) {
+      TRY(heads(*out, N, D, "q_out", &a.q_out_row, &a.q_out_head));
+      WANT(out->size(1) == q->size(1) && out->scalar_type() == q->scalar_type(),
+           "q_out: q's shape and type are wanted");
+      a.q_out = out->mutable_data_ptr();
+    } else {
+      made = at::empty({N, q->size(1), D}, q->options());
+      a.q_out_row = q->size(1) * D;
+      a.q_out_head = D;
+      a.q_out = made.mutable_data_ptr();
+    }
+  } else {
+    WANT(!out, "q_out without q");
+  }
+  if (seq) {
+    TRY(ints(*seq, 1, "seq"));
+    WANT(seq->size(0) == N, "seq: [%lld] is wanted", (long long)N);
+    a.seq = (const int32_t*)seq->const_data_ptr();
+  }
+  a.pos = (const int32_t*)pos->const_data_ptr();
+  a.page_table = (const int32_t*)table->const_data_ptr();
+  a.table_ld = table->stride(0);
+  a.n_seqs = (int)table->size(0);
+  a.max_pages = (int)table->size(1);
+  if (cos || sin) {
+    WANT(cos && sin && cos->is_cuda() && sin->is_cuda() && cos->dim() == 2 &&
+             cos->sizes() == sin->sizes() && cos->scalar_type() == at::kFloat &&
+             sin->scalar_type() == at::kFloat && cos->is_contiguous() && sin->is_contiguous(),
+         "cos, sin: both contiguous fp32 [max_pos, rot / 2] on the GPU are wanted");
+    TRY(fits(cos->size(0), "cos") && fits(2 * cos->size(1), "cos"));
+    a.cos = (const float*)cos->const_data_ptr();
+    a.sin = (const float*)sin->const_data_ptr();
+    a.max_pos = (int)cos->size(0);
+    a.rot = (int)(2 * cos->size(1));
+  }
+  a.interleaved = PyObject_IsTrue(o[9]);
+  const moe_status st = f_append(&a, at_.stream);
+  if (st != MOE_OK) return fail("kvcache_append", st);
+  return wrap(made, o[10]);
+  END_HANDLE_TH_ERRORS
+}
+
+// attend(address of the handle's kvcache_attend_args, q, page_table, seq_lens, scale or
+//        None, window, softcap, out, lse, return_lse)
+PyObject* attend(PyObject*, PyObject* const* o, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  WANT(n == 10, "10 arguments are wanted");
+  const void* base = PyLong_AsVoidPtr(o[0]);
+  TRY(base);
+  kvcache_attend_args a = *(const kvcache_attend_args*)base;  // with the default scale
+  const Tensor *q, *table, *lens, *out, *lse;
+  TRY(take_needed(o[1], "q", &q) && take_needed(o[2], "page_table", &table) &&
+      take_needed(o[3], "seq_lens", &lens) && take(o[7], "out", &out) && take(o[8], "lse", &lse));
+  WANT(q->dim() == 3, "q: [B, heads, %d] on the GPU is wanted", a.c.D);
+  const int64_t B = q->size(0), Hq = q->size(1), D = a.c.D;
+  TRY(heads(*q, B, D, "q", &a.q_row, &a.q_head));
+  TRY(ints(*table, 2, "page_table") && ints(*lens, 1, "seq_lens"));
+  WANT(table->size(0) == B && lens->size(0) == B, "page_table, seq_lens: %lld rows are wanted",
+       (long long)B);
+  TRY(fits(B, "B") && fits(Hq, "q") && fits(table->size(1), "page_table"));
+  Place at_(*q);
+  Tensor made, made_lse;
+  if (out) {
+    TRY(heads(*out, B, D, "out", &a.out_row, &a.out_head));
+    WANT(out->size(1) == Hq && out->scalar_type() == q->scalar_type(),
+         "out: q's shape and type are wanted");
+    a.out = out->mutable_data_ptr();
+  } else {
+    made = at::empty({B, Hq, D}, q->options());
+    a.out_row = Hq * D;
+    a.out_head = D;
+    a.out = made.mutable_data_ptr();
+  }
+  const bool with_lse = lse || PyObject_IsTrue(o[9]);
+  if (lse) {
+    WANT(lse->is_cuda() && lse->scalar_type() == at::kFloat && lse->dim() == 2 &&
+             lse->size(0) == B && lse->size(1) == Hq && lse->is_contiguous(),
+         "lse: contiguous fp32 [B, Hq] on the GPU is wanted");
+    a.lse = (float*)lse->mutable_data_ptr();
+  } else if (with_lse) {
+    made_lse = at::empty({B, Hq}, q->options().dtype(at::kFloat));
+    a.lse = (float*)made_lse.mutable_data_ptr();
+  }
+  a.B = (int)B;
+  a.Hq = (int)Hq;
+  a.dtype = type_code(q->scalar_type());
+  a.q = q->const_data_ptr();
+  a.page_table = (const int32_t*)table->const_data_ptr();
+  a.table_ld = table->stride(0);
+  a.max_pages = (int)table->size(1);
+  a.seq_lens = (const int32_t*)lens->const_data_ptr();
+  if (o[4] != Py_None) TRY(real(o[4], &a.scale));
+  TRY(whole(o[5], &a.window) && real(o[6], &a.softcap));
+  const moe_status st = f_attend(&a, at_.stream);
+  if (st != MOE_OK) return fail("kvcache_attend", st);
+  PyObject* result = wrap(made, o[7]);
+  return with_lse ? pair(result, wrap(made_lse, o[8])) : result;
+  END_HANDLE_TH_ERRORS
+}
+
+// w4_linear(address of the handle's moe_w4_linear_args, x, y)
+PyObject* w4_linear(PyObject*, PyObject* const* o, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  WANT(n == 3, "3 arguments are wanted");
+  const void* base = PyLong_AsVoidPtr(o[0]);
+  TRY(base);
+  moe_w4_linear_args a = *(const moe_w4_linear_args*)base;
+  const Tensor *x, *y;
+  TRY(take_needed(o[1], "x", &x) && take(o[2], "y", &y));
+  WANT(x->is_cuda() && x->dim() == 2 && type_code(x->scalar_type()) == a.dtype,
+       "x: [T, %d] of the scales' type on the GPU is wanted", a.K);
+  const int64_t T = x->size(0);
+  TRY(fits(T, "T") && rows(*x, T, a.K, "x", &a.ldx));
+  Place at_(*x);
+  Tensor made;
+  a.ldy = a.N;
+  if (y) {
+    WANT(y->scalar_type() == x->scalar_type(), "y: x's type is wanted");
+    TRY(rows(*y, T, a.N, "y", &a.ldy));
+    a.y = y->mutable_data_ptr();
+  } else {
+    made = at::empty({T, a.N}, x->options());
+    a.y = made.mutable_data_ptr();
+  }
+  a.T = (int)T;
+  a.x = x->const_data_ptr();
+  const moe_status st = f_w4(&a, at_.stream);
+  if (st != MOE_OK) return fail("moe_w4_linear", st);
+  return wrap(made, o[2]);
+  END_HANDLE_TH_ERRORS
+}
+
+// bind(the four functions' addresses in the order of moe.h, MoeError)
+PyObject* bind(PyObject*, PyObject* const* o, Py_ssize_t n) {
+  WANT(n == 5, "5 arguments are wanted");
+  void* f[4];
+  for (int i = 0; i < 4; ++i) TRY(f[i] = PyLong_AsVoidPtr(o[i]));
+  f_norm = (decltype(f_norm))f[0];
+  f_append = (decltype(f_append))f[1];
+  f_attend = (decltype(f_attend))f[2];
+  f_w4 = (decltype(f_w4))f[3];
+  Py_INCREF(o[4]);
+  Py_XDECREF(moe_error);
+  moe_error = o[4];
+  Py_RETURN_NONE;
+}
+
+#define FAST(f) (PyCFunction)(void (*)(void)) f, METH_FASTCALL
+PyMethodDef methods[] = {{"bind", FAST(bind), nullptr},
+                         {"block_norm", FAST(block_norm), nullptr},
+                         {"append", FAST(append), nullptr},
+                         {"attend", FAST(attend), nullptr},
+                         {"w4_linear", FAST(w4_linear), nullptr},
+                         {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_block", nullptr, -1, methods};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__block(void) { return PyModule_Create(&module); }
