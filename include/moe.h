@@ -682,8 +682,13 @@ moe_status kvcache_attend(const kvcache_attend_args* a, void* stream);
  * Codes and zeros hold two entries a byte, entry 2j in the low nibble of byte
  * j, rows contiguous and starting on a byte: codes [N][K/2], zeros
  * [N][ceil(K/group / 2)].  scales [N][K/group], bias and x, y of `dtype`.
- * Products are exact and sums fp32.  Meant for few tokens: the weights are
- * read once for every 16 of them.
+ * Sums are fp32.  x meets the codes in f16: a bf16 x (and any x of U4 codes)
+ * under a power of two for each 256 values of a token that brings the largest of
+ * them to [2^14, 2^15), so a product is exact unless its x is 2^-29 or more below
+ * that largest value; U4 zero points come off as sum code x - zero sum x.  An x
+ * that is infinite or NaN makes its token's results NaN or infinite.
+ * Meant for few tokens: the weights are read once for every 16 of them.  Calls that
+ * share a workspace must not overlap on the GPU.
  * K a multiple of group, group a multiple of 32; codes and x 16-byte aligned,
  * ldx a multiple of 8; else MOE_ERR_UNSUPPORTED.  T == 0 is a no-op. */
 enum { MOE_W4_U4 = 0, MOE_W4_E2M1 = 1 };
@@ -698,8 +703,13 @@ typedef struct {
   const uint8_t* zeros;            /* device or NULL                              */
   const void* bias;                /* device [N] or NULL                          */
   void* y; int64_t ldy;            /* device out [T][N]                           */
+  void* workspace;                 /* device scratch, 16-byte aligned, of
+                                      moe_w4_linear_workspace_bytes(...) (may be
+                                      NULL where that is 0: up to 8 tokens)        */
+  size_t workspace_bytes;
 } moe_w4_linear_args;
 
+size_t moe_w4_linear_workspace_bytes(int T, int K, int dtype, int format);
 moe_status moe_w4_linear(const moe_w4_linear_args* a, void* stream);
 
 #ifdef __cplusplus

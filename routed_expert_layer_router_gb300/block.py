@@ -30,7 +30,7 @@ def _address(name: str) -> int:
 
 
 _block.bind(_address("moe_block_norm"), _address("kvcache_append"), _address("kvcache_attend"),
-            _address("moe_w4_linear"), moe.MoeError)
+            _address("moe_w4_linear"), _address("moe_w4_linear_workspace_bytes"), moe.MoeError)
 
 
 def _on(stream):
@@ -160,7 +160,7 @@ class W4Linear:
     """y = x W^T + bias with 4-bit weights (moe_w4_linear): codes [N, K / 2]
     uint8 (value 2j in the low nibble), scales [N, K / group] of x's type;
     fmt "u4" (minus zeros, [N, ceil(K / group / 2)] uint8 nibbles, or 8) or
-    "e2m1".  Holds its tensors; no workspace."""
+    "e2m1".  Holds its tensors; a call takes its scratch from torch."""
 
     def __init__(self, codes, scales, group: int, zeros=None, bias=None, fmt="u4"):
         if fmt not in _FORMATS:

@@ -508,10 +508,12 @@ cudaError_t dispatch(const NormArgs& a, int vec, cudaStream_t s) {
     return launch<RT, BT, 8, 4, 1024>(a, s);
   }
   if (vec == 2) {
+    if (H <= 2 * 1024 && a.T <= 2 * kSMs) return launch<RT, BT, 2, 1, 1024>(a, s);
     if (H <= 2 * 2 * 1024) return launch<RT, BT, 2, 2, 1024>(a, s);
     if (H <= 2 * 4 * 1024) return launch<RT, BT, 2, 4, 1024>(a, s);
     return launch<RT, BT, 2, 16, 1024>(a, s);
   }
+  if (H <= 1024 && a.T <= 2 * kSMs) return launch<RT, BT, 1, 1, 1024>(a, s);
   if (H <= 4 * 1024) return launch<RT, BT, 1, 4, 1024>(a, s);
   if (H <= 8 * 1024) return launch<RT, BT, 1, 8, 1024>(a, s);
   return launch<RT, BT, 1, 32, 1024>(a, s);

@@ -26,6 +26,7 @@ moe_status (*f_norm)(const moe_block_norm_args*, void*);
 moe_status (*f_append)(const kvcache_append_args*, void*);
 moe_status (*f_attend)(const kvcache_attend_args*, void*);
 moe_status (*f_w4)(const moe_w4_linear_args*, void*);
+size_t (*f_w4_bytes)(int, int, int, int);
 PyObject* moe_error;  // MoeError(call, status)
 
 #define WANT(ok, ...)                          \
@@ -402,24 +403,32 @@ PyObject* w4_linear(PyObject*, PyObject* const* o, Py_ssize_t n) {
   }
   a.T = (int)T;
   a.x = x->const_data_ptr();
+  // scratch of this call's stream: free for the next work on it once this is done
+  Tensor scratch;
+  a.workspace_bytes = f_w4_bytes(a.T, a.K, a.dtype, a.format);
+  if (a.workspace_bytes) {
+    scratch = at::empty({(int64_t)a.workspace_bytes}, x->options().dtype(at::kByte));
+    a.workspace = scratch.mutable_data_ptr();
+  }
   const moe_status st = f_w4(&a, at_.stream);
   if (st != MOE_OK) return fail("moe_w4_linear", st);
   return wrap(made, o[2]);
   END_HANDLE_TH_ERRORS
 }
 
-// bind(the four functions' addresses in the order of moe.h, MoeError)
+// bind(the functions' addresses in the order below, MoeError)
 PyObject* bind(PyObject*, PyObject* const* o, Py_ssize_t n) {
-  WANT(n == 5, "5 arguments are wanted");
-  void* f[4];
-  for (int i = 0; i < 4; ++i) TRY(f[i] = PyLong_AsVoidPtr(o[i]));
+  WANT(n == 6, "6 arguments are wanted");
+  void* f[5];
+  for (int i = 0; i < 5; ++i) TRY(f[i] = PyLong_AsVoidPtr(o[i]));
   f_norm = (decltype(f_norm))f[0];
   f_append = (decltype(f_append))f[1];
   f_attend = (decltype(f_attend))f[2];
   f_w4 = (decltype(f_w4))f[3];
-  Py_INCREF(o[4]);
+  f_w4_bytes = (decltype(f_w4_bytes))f[4];
+  Py_INCREF(o[5]);
   Py_XDECREF(moe_error);
-  moe_error = o[4];
+  moe_error = o[5];
   Py_RETURN_NONE;
 }
 

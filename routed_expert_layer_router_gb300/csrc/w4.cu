@@ -12,6 +12,11 @@ moe_status w4_f16(const W4Args& a, int format, cudaStream_t s);  // w4_f16.cu
 
 using namespace moe;
 
+MOE_API size_t moe_w4_linear_workspace_bytes(int T, int K, int dtype, int format) {
+  if (T <= 8 || K <= 0 || (dtype == MOE_DT_F16 && format == MOE_W4_E2M1)) return 0;
+  return (size_t)((K + kChunk - 1) / kChunk) * T * kXPitch;
+}
+
 MOE_API moe_status moe_w4_linear(const moe_w4_linear_args* a, void* stream) {
   if (!a || a->T < 0 || a->N <= 0 || a->K <= 0 || a->group <= 0) return MOE_ERR_INVALID_ARG;
   if (a->format != MOE_W4_U4 && a->format != MOE_W4_E2M1) return MOE_ERR_INVALID_ARG;
@@ -23,12 +28,16 @@ MOE_API moe_status moe_w4_linear(const moe_w4_linear_args* a, void* stream) {
     return MOE_ERR_INVALID_ARG;
   if (((uintptr_t)a->x & 15) || ((uintptr_t)a->codes & 15) || a->ldx % 8)
     return MOE_ERR_UNSUPPORTED;
-  if (a->T > kTokens * 65535) return MOE_ERR_UNSUPPORTED;
+  if (a->T > kTokens * 16384) return MOE_ERR_UNSUPPORTED;
+  const size_t need = moe_w4_linear_workspace_bytes(a->T, a->K, a->dtype, a->format);
+  if (need && (!a->workspace || a->workspace_bytes < need)) return MOE_ERR_INVALID_ARG;
+  if (need && ((uintptr_t)a->workspace & 15)) return MOE_ERR_UNSUPPORTED;
   W4Args k;
   k.T = a->T, k.N = a->N, k.K = a->K, k.G = a->K / a->group, k.g32 = a->group / 32;
   k.zrow = a->zeros ? (k.G + 1) / 2 : 0;
   k.x = (const uint16_t*)a->x, k.codes = a->codes, k.scales = (const uint16_t*)a->scales;
   k.zeros = a->zeros, k.bias = (const uint16_t*)a->bias, k.y = (uint16_t*)a->y;
+  k.prepared = (uint8_t*)a->workspace;
   k.ldx = a->ldx, k.ldy = a->ldy;
   cudaStream_t s = (cudaStream_t)stream;
   return a->dtype == MOE_DT_BF16 ? w4_bf16(k, a->format, s) : w4_f16(k, a->format, s);

@@ -101,7 +101,8 @@ class kvcache_attend_args(ctypes.Structure):
 class moe_w4_linear_args(ctypes.Structure):
     _fields_ = [("T", i32), ("N", i32), ("K", i32), ("group", i32), ("dtype", i32),
                 ("format", i32), ("x", vp), ("ldx", i64), ("codes", vp), ("scales", vp),
-                ("zeros", vp), ("bias", vp), ("y", vp), ("ldy", i64)]
+                ("zeros", vp), ("bias", vp), ("y", vp), ("ldy", i64), ("workspace", vp),
+                ("workspace_bytes", sz)]
 
 
 # every function declared in include/moe.h: name -> (restype, argtypes)
@@ -140,6 +141,7 @@ SIGNATURES = {
     "kvcache_append": (i32, [ctypes.POINTER(kvcache_append_args), vp]),
     "kvcache_attend_workspace_bytes": (sz, [i32, i32, i32]),
     "kvcache_attend": (i32, [ctypes.POINTER(kvcache_attend_args), vp]),
+    "moe_w4_linear_workspace_bytes": (sz, [i32, i32, i32, i32]),
     "moe_w4_linear": (i32, [ctypes.POINTER(moe_w4_linear_args), vp]),
 }
 
@@ -353,6 +355,10 @@ def kvcache_attend_workspace_bytes(Hq: int, Hkv: int, D: int) -> int:
 
 def kvcache_attend(args: kvcache_attend_args, stream: int = 0) -> None:
     _ck("kvcache_attend", lib().kvcache_attend(ctypes.byref(args), stream))
+
+
+def moe_w4_linear_workspace_bytes(T: int, K: int, dtype: int, fmt: int) -> int:
+    return int(lib().moe_w4_linear_workspace_bytes(T, K, dtype, fmt))
 
 
 def moe_w4_linear(args: moe_w4_linear_args, stream: int = 0) -> None:

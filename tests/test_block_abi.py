@@ -130,7 +130,8 @@ def w4_args(moe, **kw):
     (dict(format=1, zeros=P), 1), (dict(x=None), 1), (dict(codes=None), 1), (dict(scales=None), 1),
     (dict(y=None), 1), (dict(ldx=255), 1), (dict(ldy=39), 1), (dict(dtype=1), 2),
     (dict(group=16), 2), (dict(group=96), 2), (dict(x=P + 2), 2), (dict(codes=P + 1), 2),
-    (dict(ldx=260), 2), (dict(T=0), 0)])
+    (dict(ldx=260), 2), (dict(T=9), 1), (dict(T=9, workspace=P, workspace_bytes=9 * 576 - 1), 1),
+    (dict(T=9, workspace=P + 8, workspace_bytes=9 * 576), 2), (dict(T=0), 0)])
 def test_w4(moe, kw, st):
     assert moe.lib().moe_w4_linear(ctypes.byref(w4_args(moe, **kw)), None) == st
 
@@ -143,3 +144,10 @@ def test_null_arguments_and_sizes(moe):
     assert L.kvcache_attend_workspace_bytes(4, 0, 64) == 0
     assert L.kvcache_attend_workspace_bytes(4, 2, 257) == 0
     assert L.kvcache_attend_workspace_bytes(4, 2, 64) > 4096
+    # 256 values of a token with their sums: 576 bytes; none up to 8 tokens, nor for
+    # f16 with E2M1 codes
+    assert L.moe_w4_linear_workspace_bytes(8, 6144, 0, 0) == 0
+    assert L.moe_w4_linear_workspace_bytes(9, 6144, 0, 0) == 9 * 24 * 576
+    assert L.moe_w4_linear_workspace_bytes(9, 6160, 0, 1) == 9 * 25 * 576
+    assert L.moe_w4_linear_workspace_bytes(9, 6144, 2, 0) == 9 * 24 * 576
+    assert L.moe_w4_linear_workspace_bytes(9, 6144, 2, 1) == 0
