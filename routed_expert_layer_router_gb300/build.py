@@ -34,7 +34,7 @@ def _block_command() -> list:
             "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
             "-isystem", os.path.join(cuda, "include"),
             os.path.join(CSRC, "torch_block.cpp"), "-o", BLOCK, "-L" + lib, "-Wl,-rpath," + lib,
-            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
 
 
 def build(verbose: bool = False, ptxas_verbose: bool = False) -> str:

@@ -3,14 +3,14 @@
 // the outputs a caller did not give, fills the call's structure and calls the
 // library on the current stream; block.py holds the documented functions and
 // classes over it.  (The same in Python over ctypes costs 12 us a call on a
-// Grace core against REPLACE here, and several of the kernels take 2.)
+// Grace core against 3.1 to 5.1 here, and several of the kernels take 2.)
 //
 // The library's functions and its Python exception come in through bind().
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -146,6 +146,10 @@ PyObject* fail(const char* call, moe_status st) {
   Py_XDECREF(args);
   return nullptr;
 }
+// an output of the current stream, on the device of `like`
+Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const Tensor& like) {
+  return Tensor(at::detail::empty_cuda(shape, type, like.device(), std::nullopt));
+}
 PyObject* wrap(const Tensor& made, PyObject* given) {
   if (given != Py_None) {
     Py_INCREF(given);
@@ -230,14 +234,14 @@ PyObject* block_norm(PyObject*, PyObject* const* o, Py_ssize_t n) {
     TRY(rows(*r, T, H, "r", &a.ldr));
     a.r = r->mutable_data_ptr();
   } else if (PyObject_IsTrue(o[16])) {
-    made_r = at::empty({T, H}, x->options());
+    made_r = fresh({T, H}, x->scalar_type(), *x);
     a.r = made_r.mutable_data_ptr();
   }
   if (h) {
     TRY(rows(*h, T, H, "h", &a.ldh));
     a.h = h->mutable_data_ptr();
   } else if (PyObject_IsTrue(o[17])) {
-    made_h = at::empty({T, H}, x->options().dtype(branch));
+    made_h = fresh({T, H}, branch, *x);
     a.h = made_h.mutable_data_ptr();
   }
   const moe_status st = f_norm(&a, at_.stream);
@@ -283,7 +287,7 @@ PyObject* append(PyObject*, PyObject* const* o, Py_ssize_t n) {
            "q_out: q's shape and type are wanted");
       a.q_out = out->mutable_data_ptr();
     } else {
-      made = at::empty({N, q->size(1), D}, q->options());
+      made = fresh({N, q->size(1), D}, q->scalar_type(), *q);
       a.q_out_row = q->size(1) * D;
       a.q_out_head = D;
       a.q_out = made.mutable_data_ptr();
@@ -345,7 +349,7 @@ PyObject* attend(PyObject*, PyObject* const* o, Py_ssize_t n) {
          "out: q's shape and type are wanted");
     a.out = out->mutable_data_ptr();
   } else {
-    made = at::empty({B, Hq, D}, q->options());
+    made = fresh({B, Hq, D}, q->scalar_type(), *q);
     a.out_row = Hq * D;
     a.out_head = D;
     a.out = made.mutable_data_ptr();
@@ -357,7 +361,7 @@ PyObject* attend(PyObject*, PyObject* const* o, Py_ssize_t n) {
          "lse: contiguous fp32 [B, Hq] on the GPU is wanted");
     a.lse = (float*)lse->mutable_data_ptr();
   } else if (with_lse) {
-    made_lse = at::empty({B, Hq}, q->options().dtype(at::kFloat));
+    made_lse = fresh({B, Hq}, at::kFloat, *q);
     a.lse = (float*)made_lse.mutable_data_ptr();
   }
   a.B = (int)B;
@@ -398,7 +402,7 @@ PyObject* w4_linear(PyObject*, PyObject* const* o, Py_ssize_t n) {
     TRY(rows(*y, T, a.N, "y", &a.ldy));
     a.y = y->mutable_data_ptr();
   } else {
-    made = at::empty({T, a.N}, x->options());
+    made = fresh({T, a.N}, x->scalar_type(), *x);
     a.y = made.mutable_data_ptr();
   }
   a.T = (int)T;
@@ -407,7 +411,7 @@ PyObject* w4_linear(PyObject*, PyObject* const* o, Py_ssize_t n) {
   Tensor scratch;
   a.workspace_bytes = f_w4_bytes(a.T, a.K, a.dtype, a.format);
   if (a.workspace_bytes) {
-    scratch = at::empty({(int64_t)a.workspace_bytes}, x->options().dtype(at::kByte));
+    scratch = fresh({(int64_t)a.workspace_bytes}, at::kByte, *x);
     a.workspace = scratch.mutable_data_ptr();
   }
   const moe_status st = f_w4(&a, at_.stream);

@@ -28,7 +28,7 @@ MOE_API moe_status moe_w4_linear(const moe_w4_linear_args* a, void* stream) {
     return MOE_ERR_INVALID_ARG;
   if (((uintptr_t)a->x & 15) || ((uintptr_t)a->codes & 15) || a->ldx % 8)
     return MOE_ERR_UNSUPPORTED;
-  if (a->T > kTokens * 16384) return MOE_ERR_UNSUPPORTED;
+  if (a->T > 4 * 65535) return MOE_ERR_UNSUPPORTED;  // the grids' second dimension
   const size_t need = moe_w4_linear_workspace_bytes(a->T, a->K, a->dtype, a->format);
   if (need && (!a->workspace || a->workspace_bytes < need)) return MOE_ERR_INVALID_ARG;
   if (need && ((uintptr_t)a->workspace & 15)) return MOE_ERR_UNSUPPORTED;
