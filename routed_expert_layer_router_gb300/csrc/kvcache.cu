@@ -150,11 +150,11 @@ __global__ void __launch_bounds__(kAppendThreads, 4)
 // the GPU alike.  In a CTA each of 4 warps streams its 16 or 32 tokens of a tile
 // through its own ring of cp.async stages (a token's place in its page is found
 // for each token, so pages of any size run alike; no barrier between warps inside
-// an item) and keeps a running maximum, sum and output in registers.  The query heads of a kv head are the rows of the matrix
-// instructions, so K and V are read once for all of them.  A run that covers an
-// item writes its result; items cut between CTAs leave their parts in the
-// workspace, and the CTA that finishes last adds them (in an order of the parts,
-// so the same bits every time).
+// an item) and keeps a running maximum, sum and output in registers.  The query
+// heads of a kv head are the rows of the matrix instructions, so K and V are read
+// once for all of them.  A run that covers an item writes its result; items cut
+// between CTAs leave their parts in the workspace, and the CTA that finishes last
+// adds them (in an order of the parts, so the same bits every time).
 // (TMA boxes of a page's tokens, one per warp and stage, were measured slower:
 // 98 against 86 us at 1 x 131075 tokens of 8 x 128 values in bf16.)
 constexpr int kWarps = 4;
@@ -255,6 +255,9 @@ __global__ void __launch_bounds__(kWarps * 32, Ring<KV, DP, RH>::CTAS) k_attend(
   constexpr int TOK = R::TOK, TILE = R::TILE, TT = TOK / 8;  // TT: score tiles of 8 tokens
   constexpr int ROWS = 8 * RH, SLICE = ROWS * DP, PART = ROWS * (DP + 2);
   constexpr uint32_t ALL = TOK == 32 ? ~0u : 0xffffu;
+  // Weights are kept times 2^LIFT: f16 would drop those 2^-25 below a row's largest,
+  // and a hundred thousand of them count.  The largest is then 2^15 of f16's 65504.
+  constexpr float LIFT = MT == MOE_DT_F16 ? 15.f : 0.f;
   static_assert(SLICE * 4 <= R::WARP, "a warp's sums fit its part of a stage");
   extern __shared__ __align__(128) uint8_t ring[];
   float* mb = (float*)(ring + R::BYTES);  // merge buffer: RH 1: two slices of 8 rows, 2: one of 16
@@ -545,7 +548,7 @@ __global__ void __launch_bounds__(kWarps * 32, Ring<KV, DP, RH>::CTAS) k_attend(
           ((uint4*)dst)[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
           ((uint4*)dst)[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
           if (p == 0 && a.lse)
-            a.lse[(int64_t)cc.b * a.Hq + kvh * a.G + head] = (st.x + log2f(st.y)) * (1.f / kLog2e);
+            a.lse[(int64_t)cc.b * a.Hq + kvh * a.G + head] = (st.x + (log2f(st.y) - LIFT)) * (1.f / kLog2e);
         }
         __syncthreads();
         return;
@@ -717,7 +720,7 @@ __global__ void __launch_bounds__(kWarps * 32, Ring<KV, DP, RH>::CTAS) k_attend(
       for (int i = 0; i < TT; ++i) top = fmaxf(top, fmaxf(s[i][2 * r], s[i][2 * r + 1]));
       top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
       top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-      const float z = zero_if_empty(top);
+      const float z = zero_if_empty(top), lifted = z - LIFT;
       al[r] = exp2_approx(m[r] - z);
       grew |= top != m[r];
       m[r] = top;
@@ -726,7 +729,7 @@ __global__ void __launch_bounds__(kWarps * 32, Ring<KV, DP, RH>::CTAS) k_attend(
       for (int i = 0; i < TT; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          s[i][2 * r + j] = exp2_approx(s[i][2 * r + j] - z);
+          s[i][2 * r + j] = exp2_approx(s[i][2 * r + j] - lifted);
           sum += s[i][2 * r + j];
         }
       l[r] = l[r] * al[r] + sum;
@@ -828,7 +831,7 @@ moe_status launch_attend(AttendArgs a, cudaStream_t s) {
   // tiles there can be: counted in 32 bits on the device
   const int64_t tiles = ((int64_t)a.cap + R::TILE - 1) / R::TILE + 1;
   const double most = (double)a.B * a.c.Hkv * a.nhb * (double)tiles;
-  if (most >= 2147483648.0) return MOE_ERR_UNSUPPORTED;
+  if (most >= 1073741824.0) return MOE_ERR_UNSUPPORTED;
   const int resident = R::CTAS * kSMs;
   const int grid = most < resident ? (int)most : resident;
   return launch_status(launch_pdl(k_attend<KV, DP, RH>, grid, kWarps * 32, smem, s, a));

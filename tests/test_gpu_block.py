@@ -367,6 +367,21 @@ def test_attend_large_scores(block):
         assert torch.isfinite(out).all()
 
 
+@pytest.mark.parametrize("dtype,kv", [(F16, F16), (BF, F8), (BF, BF)])
+def test_attend_many_small_weights(block, dtype, kv):
+    """A token whose weight is 2^26 times every other's: the others' values still
+    count, for there are 100000 of them (each below f16's smallest number)."""
+    n, page, D = 100000, 50, 16
+    k = torch.zeros(n // page, 1, page, D, device="cuda")
+    v = torch.ones_like(k)
+    k[0, 0, 7, 0], v[0, 0, 7] = 1.0, 0.0
+    q = torch.zeros(1, 2, D, device="cuda")
+    q[..., 0] = 18.0
+    table = torch.arange(n // page, dtype=torch.int32, device="cuda")[None]
+    check_attend(block, q.to(dtype), k.to(kv), v.to(kv), table, [n],
+                 *([torch.ones(1, device="cuda")] * 2 if kv == F8 else []), scale=1.0)
+
+
 def test_attend_bad_pages_and_lengths(block):
     g, Hkv, D, page = gen(9), 2, 64, 16
     lens = [100, 50, 33]
