@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kWarps * 32, Ring<KV, DP, RH>::CTAS) k_attend(
   static_assert(SLICE * 4 <= R::WARP, "a warp's sums fit its part of a stage");
   extern __shared__ __align__(128) uint8_t ring[];
   float* mb = (float*)(ring + R::BYTES);  // merge buffer: RH 1: two slices of 8 rows, 2: one of 16
-  __shared__ float2 ml[kWarps][ROWS];
+  __shared__ float2 mls[2][kWarps][ROWS];  // two items': no barrier after an item's output
   __shared__ uint32_t valid[kWarps][S];
   __shared__ int is_last;
 
@@ -389,20 +389,16 @@ __global__ void __launch_bounds__(kWarps * 32, Ring<KV, DP, RH>::CTAS) k_attend(
     cp_async_commit();
   };
 
-  // ---- queries of an item, as matrix operands
+  // ---- queries of an item, as matrix operands: their loads leave before the end of
+  // the item before
   uint32_t qa[KS][2 * RH];
-  float acc[NT][4], m[RH], l[RH], sc[RH];
-  auto begin_item = [&]() {
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+  float acc[NT][4], m[RH], l[RH], sc[RH], ks = 1.f;
+  const bool full = a.c.D > DP / 4 * 3;  // else the last quarter of DP is not computed
+  auto load_item = [&]() {
     const int kvh = cc.h / a.nhb, hb = cc.h - kvh * a.nhb;
-    const float ks = KV == MOE_DT_E4M3 && a.c.k_scale ? a.c.k_scale[kvh] : 1.f;
+    if (KV == MOE_DT_E4M3 && a.c.k_scale) ks = a.c.k_scale[kvh];
 #pragma unroll
     for (int r = 0; r < RH; ++r) {
-      m[r] = NEG_INF;
-      l[r] = 0.f;
       const int row = hb * ROWS + r * 8 + g;
       const bool on = row < a.G;
       const uint16_t* q =
@@ -422,6 +418,17 @@ __global__ void __launch_bounds__(kWarps * 32, Ring<KV, DP, RH>::CTAS) k_attend(
         qa[s][r] = x;
         qa[s][RH + r] = y;
       }
+    }
+  };
+  auto begin_item = [&]() {
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+#pragma unroll
+    for (int r = 0; r < RH; ++r) {
+      m[r] = NEG_INF;
+      l[r] = 0.f;
       float back = 1.f;
       if (KV == MOE_DT_E4M3 && a.q_bf16) {
         // keys are held in f16 (exact for E4M3), so a bf16 query goes to f16
@@ -453,10 +460,13 @@ __global__ void __launch_bounds__(kWarps * 32, Ring<KV, DP, RH>::CTAS) k_attend(
     }
   };
 
-  // ---- the end of an item: t0, t1: the tiles of it that this run covered; first_u:
+  // ---- the end of item `it`: t0, t1: the tiles of it that this run covered; first_u:
   // its first tile among all; idle: the ring has nothing left to bring
   auto zero_if_empty = [](float M) { return M == NEG_INF ? 0.f : M; };
-  auto end_item = [&](int first_u, int t0, int t1, bool idle) {
+  int flip = 0;
+  auto end_item = [&](const Cursor<TILE>& it, int first_u, int t0, int t1, bool idle) {
+    float2 (*ml)[ROWS] = mls[flip];
+    flip ^= 1;
     auto stat = [&](int row) {  // (maximum, sum) of a row over the warps
       float M = ml[0][row].x, L = 0.f;
 #pragma unroll
@@ -485,14 +495,14 @@ __global__ void __launch_bounds__(kWarps * 32, Ring<KV, DP, RH>::CTAS) k_attend(
       }
       return x;
     };
-    const int kvh = cc.h / a.nhb, hb = cc.h - kvh * a.nhb;
+    const int kvh = it.h / a.nhb, hb = it.h - kvh * a.nhb;
 #pragma unroll
     for (int r = 0; r < RH; ++r) {
       l[r] += __shfl_xor_sync(~0u, l[r], 1);
       l[r] += __shfl_xor_sync(~0u, l[r], 2);
     }
 #pragma unroll 1
-    for (bool whole = t0 == 0 && t1 == cc.nt;; whole = true) {
+    for (bool whole = t0 == 0 && t1 == it.nt;; whole = true) {
 #pragma unroll
       for (int r = 0; r < RH; ++r)
         if (c4 == 0) ml[w][r * 8 + g] = make_float2(m[r], l[r]);
@@ -539,7 +549,7 @@ __global__ void __launch_bounds__(kWarps * 32, Ring<KV, DP, RH>::CTAS) k_attend(
                 o[d] = v[c] * k;
               }
             }
-          uint16_t* dst = (uint16_t*)a.out + cc.b * a.out_row +
+          uint16_t* dst = (uint16_t*)a.out + it.b * a.out_row +
                           (int64_t)(kvh * a.G + head) * a.out_head + p * 16;
           uint32_t pk[8];
 #pragma unroll
@@ -548,9 +558,8 @@ __global__ void __launch_bounds__(kWarps * 32, Ring<KV, DP, RH>::CTAS) k_attend(
           ((uint4*)dst)[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
           ((uint4*)dst)[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
           if (p == 0 && a.lse)
-            a.lse[(int64_t)cc.b * a.Hq + kvh * a.G + head] = (st.x + (log2f(st.y) - LIFT)) * (1.f / kLog2e);
+            a.lse[(int64_t)it.b * a.Hq + kvh * a.G + head] = (st.x + (log2f(st.y) - LIFT)) * (1.f / kLog2e);
         }
-        __syncthreads();
         return;
       }
       // part p of the item comes from run cs + p; the first is that run's last
@@ -559,7 +568,7 @@ __global__ void __launch_bounds__(kWarps * 32, Ring<KV, DP, RH>::CTAS) k_attend(
         const int longer = more * (each + 1);
         return u < longer ? u / (each + 1) : more + (u - longer) / each;
       };
-      const int cs = run_of(first_u), np = run_of(first_u + cc.nt - 1) - cs + 1;
+      const int cs = run_of(first_u), np = run_of(first_u + it.nt - 1) - cs + 1;
       auto part = [&](int p) {
         return a.parts + (size_t)(p == 0 ? 2 * cs + 1 : 2 * (cs + p)) * PART;
       };
@@ -629,13 +638,14 @@ __global__ void __launch_bounds__(kWarps * 32, Ring<KV, DP, RH>::CTAS) k_attend(
         if (u0 + i + 1 < u1) cp.next(a, nh);
       }
     }
-    begin_item();
+    load_item();
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) {
       page = pages[i];
       issue(i);
     }
     page = pages[AHEAD];
+    begin_item();
   }
   auto issue_next = [&](int stage) {
     issue(stage);
@@ -661,6 +671,7 @@ __global__ void __launch_bounds__(kWarps * 32, Ring<KV, DP, RH>::CTAS) k_attend(
         const int row = t * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
 #pragma unroll
         for (int k = 0; k < KS; k += 2) {
+          if (k >= KS / 4 * 3 && !full) break;
           uint32_t r[4];
           ldmatrix_x4(r, kd + R::at(row, k + (lane >> 4)));
 #pragma unroll
@@ -677,6 +688,7 @@ __global__ void __launch_bounds__(kWarps * 32, Ring<KV, DP, RH>::CTAS) k_attend(
         const int row = t * 16 + (lane & 7) + (lane >> 4) * 8;
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
+          if (k >= KS / 4 * 3 && !full) break;
           uint32_t r[4];
           ldmatrix_x4(r, kd + R::at(row, 2 * k + ((lane >> 3) & 1)));
           const uint32_t qf[4] = {qa[k][0], RH == 2 ? qa[k][RH - 1] : 0u, qa[k][RH],
@@ -764,6 +776,7 @@ __global__ void __launch_bounds__(kWarps * 32, Ring<KV, DP, RH>::CTAS) k_attend(
       const int row = t * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
 #pragma unroll
       for (int k = 0; k < CPR; k += 2) {
+        if (k >= CPR / 4 * 3 && !full) break;
         uint32_t r[4];
         ldmatrix_x4_trans(r, vd + R::at(row, k + (lane >> 4)));
         if constexpr (KV == MOE_DT_E4M3) {
@@ -797,9 +810,13 @@ __global__ void __launch_bounds__(kWarps * 32, Ring<KV, DP, RH>::CTAS) k_attend(
     }
     if (++stage == S) stage = 0;
     if (cc.tile + 1 == cc.nt || u + 1 == u1) {
-      end_item(u - cc.tile, t0, cc.tile + 1, u + 1 == u1);
+      const Cursor<TILE> it = cc;
       if (u + 1 < u1) {
         cc.next(a, nh);
+        load_item();
+      }
+      end_item(it, u - it.tile, t0, it.tile + 1, u + 1 == u1);
+      if (u + 1 < u1) {
         begin_item();
         t0 = 0;
       }
