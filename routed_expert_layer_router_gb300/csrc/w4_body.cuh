@@ -38,6 +38,7 @@ struct W4Args {
 namespace {
 
 constexpr int kChunk = 256;            // input values of a stage: 128 bytes of a row
+constexpr int kMostCtas = 8;           // of a cluster
 constexpr int kTokens = 16;            // tokens of one pass over the weights
 // Bytes of a token's chunk in shared memory and in the workspace: its 256 values
 // (prepared: f16), its 8 group sums, and what undoes its power of two.  The 64
@@ -140,11 +141,11 @@ __device__ __forceinline__ void cluster_sync() {
 // fp32 at the address of this CTA's shared memory, read from CTA `rank` of the cluster
 __device__ __forceinline__ float cluster_load(uint32_t addr, uint32_t rank) {
   float v;
+  // no clobber: the loads of several CTAs may leave together, between two barriers
   asm volatile("{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %1, %2;\n"
                " ld.shared::cluster.f32 %0, [a];\n}"
                : "=f"(v)
-               : "r"(addr), "r"(rank)
-               : "memory");
+               : "r"(addr), "r"(rank));
   return v;
 }
 
@@ -213,6 +214,39 @@ __global__ void __launch_bounds__(256, Shape<NT, WR>::PER_SM) k_w4(W4Args a) {
   const uint32_t cdst1 = cring + r0 * 128 + ((lane & 7) ^ (r0 + 4)) * 16;  // r0 + 4, r0 + 12, ...
   const uint16_t* xsrc = a.x + (t0 + min(wr, nt - 1)) * a.ldx + lane * 8;
   const uint32_t xdst = ptx::smem_u32(xbase) + wr * kXPitch + lane * 16;
+  // Scale and zero point of the warp's rows h * 8 + g and a group: with G32 the four
+  // lanes of a row fetch one group each of the next chunk (two each of eight), ahead
+  // of its work; they stay as they came until that begins, so nothing waits for them
+  const uint16_t* sp[2];
+  const uint8_t* zp[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int64_t row = min(n0 + h * 8 + g, a.N - 1);
+    sp[h] = a.scales + row * a.G + (G32 ? c4 % NG : 0);
+    zp[h] = a.zeros ? a.zeros + row * a.zrow + (G32 ? c4 % NG / 2 : 0) : nullptr;
+  }
+  uint32_t s_next[2][SV] = {}, z_next[2][SV] = {};
+  auto fetch_scales = [&](int kc) {
+    if constexpr (G32 != 0) {
+#pragma unroll
+      for (int v = 0; v < SV; ++v) {
+        if (kc * NG + v * 4 + c4 % NG >= a.G) continue;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          s_next[h][v] = sp[h][kc * NG + v * 4];
+          if (U4 && zp[h]) z_next[h][v] = zp[h][kc * (NG / 2) + v * 2];
+        }
+      }
+    }
+  };
+  // a scale in the high half, its zero point below
+  auto join = [&](uint32_t scale, uint32_t zeros, int grp, bool has) {
+    const uint32_t zero = has ? (zeros >> (4 * (grp & 1))) & 15 : 8;
+    return scale << 16 | (U4 ? zero : 0);
+  };
+  auto scale_word = [&](int h, int grp) {  // G32 == 0: at its beginning
+    return join(sp[h][grp], U4 && zp[h] ? zp[h][grp / 2] : 0, grp, zp[h]);
+  };
   auto issue_codes = [&](int kc, int stage) {
     if (kc >= chunks) return;
     const int64_t at = (int64_t)kc * (kChunk / 2);
@@ -238,6 +272,7 @@ __global__ void __launch_bounds__(256, Shape<NT, WR>::PER_SM) k_w4(W4Args a) {
         cp_async16(xd, xs, xin ? 16 : 0);
     }
   };
+  fetch_scales(first);
 #pragma unroll
   for (int i = 0; i < S; ++i) {
     issue_codes(first + i * step, i);
@@ -257,39 +292,6 @@ __global__ void __launch_bounds__(256, Shape<NT, WR>::PER_SM) k_w4(W4Args a) {
     }
   }
 
-  // Scale (high half) and zero point of the warp's rows h * 8 + g and a group: with
-  // G32 the four lanes of a row fetch one group each of the next chunk (two each
-  // of eight), ahead of its work
-  const uint16_t* sp[2];
-  const uint8_t* zp[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int64_t row = min(n0 + h * 8 + g, a.N - 1);
-    sp[h] = a.scales + row * a.G + (G32 ? c4 % NG : 0);
-    zp[h] = a.zeros ? a.zeros + row * a.zrow + (G32 ? c4 % NG / 2 : 0) : nullptr;
-  }
-  uint32_t cur[2][SV] = {}, nxt[2][SV] = {};
-  auto fetch_scales = [&](int kc) {
-    if constexpr (G32 != 0) {
-#pragma unroll
-      for (int v = 0; v < SV; ++v) {
-        if (kc * NG + v * 4 + c4 % NG >= a.G) continue;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          nxt[h][v] = (uint32_t)sp[h][kc * NG + v * 4] << 16;
-          if constexpr (FMT == MOE_W4_U4)
-            nxt[h][v] |= zp[h] ? (zp[h][kc * (NG / 2) + v * 2] >> (4 * (c4 & 1))) & 15 : 8;
-        }
-      }
-    }
-  };
-  auto scale_word = [&](int h, int grp) {  // G32 == 0: at its beginning
-    uint32_t v = (uint32_t)sp[h][grp] << 16;
-    if constexpr (FMT == MOE_W4_U4) v |= zp[h] ? (zp[h][grp / 2] >> (4 * (grp & 1))) & 15 : 8;
-    return v;
-  };
-  fetch_scales(first);
-
   float acc[NT][4] = {}, sum[NT][4];
   int stage = 0;
   auto group_sync = [&]() {  // the warps that share a chunk
@@ -304,10 +306,11 @@ __global__ void __launch_bounds__(256, Shape<NT, WR>::PER_SM) k_w4(W4Args a) {
   for (int kc = first; kc < chunks; kc += step) {
     cp_async_wait<S - 1>();
     group_sync();
+    uint32_t cur[2][SV];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int v = 0; v < SV; ++v) cur[h][v] = nxt[h][v];
+      for (int v = 0; v < SV; ++v) cur[h][v] = join(s_next[h][v], z_next[h][v], c4, zp[h]);
     fetch_scales(kc + step);
     const uint32_t cb = crow + stage * STAGE;
     const int blocks = min(8, a.K / 32 - kc * 8);  // of 32 values, in this chunk
@@ -456,11 +459,13 @@ __global__ void __launch_bounds__(256, Shape<NT, WR>::PER_SM) k_w4(W4Args a) {
     for (int q = 0; q < 4; ++q) red[(w * NT + n) * 128 + q * 32 + lane] = acc[n][q];
   __syncthreads();
   if (csize > 1) {
+    if (a.wk > 1) {
 #pragma unroll 1
-    for (int i = threadIdx.x; i < OUT; i += blockDim.x) {
-      float v = red[i];
-      for (int k = 1; k < a.wk; ++k) v += red[k * OUT + i];
-      red[i] = v;
+      for (int i = threadIdx.x; i < OUT; i += blockDim.x) {
+        float v = red[i];
+        for (int k = 1; k < a.wk; ++k) v += red[k * OUT + i];
+        red[i] = v;
+      }
     }
     cluster_sync();
   }
@@ -473,7 +478,11 @@ __global__ void __launch_bounds__(256, Shape<NT, WR>::PER_SM) k_w4(W4Args a) {
     if (row < a.N && t < nt) {
       float v = 0.f;
       if (csize > 1) {
-        for (int k = 0; k < csize; ++k) v += cluster_load(red_addr + i * 4, k);
+        float u[kMostCtas];
+#pragma unroll
+        for (int k = 0; k < kMostCtas; ++k) u[k] = k < csize ? cluster_load(red_addr + i * 4, k) : 0.f;
+#pragma unroll
+        for (int k = 0; k < kMostCtas; ++k) v += u[k];
       } else {
         for (int k = 0; k < a.wk; ++k) v += red[k * OUT + i];
       }
@@ -508,7 +517,7 @@ moe_status launch_w4(W4Args a, cudaStream_t s) {
   // do not pack (16 tokens, 6144 x 6144: 18 us in clusters of 6, 13.5 in fours)
   a.wk = 8 / WR < chunks ? 8 / WR : chunks;
   auto share = [&](int c) { return (chunks + a.wk * c - 1) / (a.wk * c); };
-  int cluster = 8;
+  int cluster = kMostCtas;
   while (cluster > 1 && ((int64_t)tiles * passes * cluster > Shape<NT, WR>::CTAS ||
                          share(cluster) == share(cluster - 1) ||
                          (NT == 2 && (cluster & (cluster - 1)))))
