@@ -14,7 +14,7 @@ using namespace moe;
 
 MOE_API size_t moe_w4_linear_workspace_bytes(int T, int K, int dtype, int format) {
   if (T <= 8 || K <= 0 || (dtype == MOE_DT_F16 && format == MOE_W4_E2M1)) return 0;
-  return (size_t)((K + kChunk - 1) / kChunk) * T * kXPitch;
+  return (size_t)((K + kChunk - 1) / kChunk) * ((T + kTokens - 1) / kTokens) * kPass;
 }
 
 MOE_API moe_status moe_w4_linear(const moe_w4_linear_args* a, void* stream) {

@@ -31,7 +31,7 @@ struct W4Args {
   const uint8_t* zeros;
   const uint16_t* bias;
   uint16_t* y;
-  uint8_t* prepared;                   // [chunk][T][kXPitch], or nullptr: prepared here
+  uint8_t* prepared;                   // [chunk][pass][17][kXPitch], or nullptr: prepared here
   int64_t ldx, ldy;
 };
 
@@ -40,11 +40,17 @@ namespace {
 constexpr int kChunk = 256;            // input values of a stage: 128 bytes of a row
 constexpr int kMostCtas = 8;           // of a cluster
 constexpr int kTokens = 16;            // tokens of one pass over the weights
-// Bytes of a token's chunk in shared memory and in the workspace: its 256 values
-// (prepared: f16), its 8 group sums, and what undoes its power of two.  The 64
-// bytes past the values also put two tokens' reads into different bank halves.
+// A chunk of x, in shared memory and in the workspace: a row of group sums and of
+// what undoes each token's power of two, then a row for each token's 256 values
+// (prepared: f16).  The 64 bytes past the values put two tokens' reads into different
+// bank halves.  A row of sums holds 8 groups (or blocks of 32) of 16 tokens, then the
+// 16 tokens' powers, the tokens in the order in which a thread of the matrix
+// instructions wants its two or four together.
 constexpr int kXPitch = kChunk * 2 + 64;
-constexpr int kSums = kChunk * 2, kUndo = kSums + 32;
+constexpr int kUndo = 8 * kTokens;
+constexpr int kPass = (kTokens + 1) * kXPitch;  // of the workspace
+static_assert((kUndo + kTokens) * 4 <= kXPitch, "a row of sums");
+__device__ __forceinline__ int sum_place(int t) { return (t & 6) * 2 + (t >> 3) * 2 + (t & 1); }
 
 // Codes reach the matrix instructions as exact f16 numbers, by as few instructions
 // as there are: E2M1 by the conversion instruction; u4 by masks alone, a nibble
@@ -105,13 +111,14 @@ __device__ __forceinline__ float prepare_x(uint4& v, float& sum) {
   return __uint_as_float((uint32_t)(127 - up) << 23);
 }
 
-// the same with the chunk's sums, into its place of kXPitch bytes; g32: the group's
-// length in blocks of 32 where it is 1, 2 or 4, else sums are of blocks
+// the same for token t of a chunk at `to`, with its sums; g32: the group's length in
+// blocks of 32 where it is 1, 2 or 4, else sums are of blocks
 template <int DT, int FMT>
-__device__ __forceinline__ void prepare_chunk(uint4 v, int g32, uint8_t* to, int lane) {
+__device__ __forceinline__ void prepare_chunk(uint4 v, int g32, uint8_t* to, int t, int lane) {
   float sum;
   const float undo = prepare_x<DT, FMT>(v, sum);
-  *(uint4*)(to + lane * 16) = v;
+  *(uint4*)(to + (t + 1) * kXPitch + lane * 16) = v;
+  float* row = (float*)to + sum_place(t);
   if constexpr (FMT == MOE_W4_U4) {
     // lanes 4 i .. 4 i + 3 hold block i
     const int per = g32 == 2 || g32 == 4 ? 4 * g32 : 4;
@@ -119,9 +126,9 @@ __device__ __forceinline__ void prepare_chunk(uint4 v, int g32, uint8_t* to, int
     sum += __shfl_xor_sync(~0u, sum, 2);
     if (per > 4) sum += __shfl_xor_sync(~0u, sum, 4);
     if (per > 8) sum += __shfl_xor_sync(~0u, sum, 8);
-    if ((lane & (per - 1)) == 0) *(float*)(to + kSums + lane / per * 4) = sum;
+    if ((lane & (per - 1)) == 0) row[lane / per * kTokens] = sum;
   }
-  if (lane == 0) *(float*)(to + kUndo) = undo;
+  if (lane == 0) row[kUndo] = undo;
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -169,8 +176,9 @@ __global__ void __launch_bounds__(128) k_w4_prepare(W4Args a) {
   const int k = kc * kChunk + lane * 8;
   uint4 v = make_uint4(0, 0, 0, 0);
   if (k < a.K) v = *(const uint4*)(a.x + t * a.ldx + k);
-  uint8_t* to = a.prepared + ((int64_t)kc * a.T + t) * kXPitch;
-  prepare_chunk<DT, FMT>(v, a.g32, to, lane);
+  const int passes = (a.T + kTokens - 1) / kTokens;
+  uint8_t* to = a.prepared + ((int64_t)kc * passes + t / kTokens) * kPass;
+  prepare_chunk<DT, FMT>(v, a.g32, to, t % kTokens, lane);
 }
 
 // PRE: x comes prepared from the workspace; the kernel that prepares it is the one
@@ -195,7 +203,7 @@ __global__ void __launch_bounds__(256, Shape<NT, WR>::PER_SM) k_w4(W4Args a) {
   const int step = a.wk * csize;            // this warp: chunks first, first + step, ...
   const int first = crank * a.wk + kw;
   const int64_t krow = a.K / 2;
-  const int xstage = nt * kXPitch;
+  const int xstage = (nt + 1) * kXPitch;
   const uint32_t cring = ptx::smem_u32(sm) + w * S * STAGE;
   uint8_t* xbase = sm + a.wk * WR * S * STAGE + kw * S * xstage;
   if constexpr (!PRE) {
@@ -213,7 +221,7 @@ __global__ void __launch_bounds__(256, Shape<NT, WR>::PER_SM) k_w4(W4Args a) {
   const uint32_t cdst0 = cring + r0 * 128 + ((lane & 7) ^ r0) * 16;        // rows r0, r0 + 8, ...
   const uint32_t cdst1 = cring + r0 * 128 + ((lane & 7) ^ (r0 + 4)) * 16;  // r0 + 4, r0 + 12, ...
   const uint16_t* xsrc = a.x + (t0 + min(wr, nt - 1)) * a.ldx + lane * 8;
-  const uint32_t xdst = ptx::smem_u32(xbase) + wr * kXPitch + lane * 16;
+  const uint32_t xdst = ptx::smem_u32(xbase) + (wr + 1) * kXPitch + lane * 16;
   // Scale and zero point of the warp's rows h * 8 + g and a group: with G32 the four
   // lanes of a row fetch one group each of the next chunk (two each of eight), ahead
   // of its work; they stay as they came until that begins, so nothing waits for them
@@ -259,7 +267,7 @@ __global__ void __launch_bounds__(256, Shape<NT, WR>::PER_SM) k_w4(W4Args a) {
   auto issue_x = [&](int kc, int stage) {
     if (kc >= chunks) return;
     if constexpr (PRE) {
-      const uint8_t* from = a.prepared + ((int64_t)kc * a.T + t0) * kXPitch;
+      const uint8_t* from = a.prepared + ((int64_t)kc * gridDim.y + blockIdx.y) * kPass;
       const uint32_t to = ptx::smem_u32(xbase) + stage * xstage;
 #pragma unroll 1
       for (int i = (wr * 32 + lane) * 16; i < xstage; i += WR * 512) cp_async16(to + i, from + i, 16);
@@ -292,16 +300,28 @@ __global__ void __launch_bounds__(256, Shape<NT, WR>::PER_SM) k_w4(W4Args a) {
     }
   }
 
-  float acc[NT][4] = {}, sum[NT][4];
+  float2 acc[NT][2] = {};
+  float sum[NT][4];
   int stage = 0;
   auto group_sync = [&]() {  // the warps that share a chunk
     if constexpr (WR == 1) __syncwarp();
     else asm volatile("bar.sync %0, %1;" ::"r"(1 + kw), "n"(WR * 32) : "memory");
   };
+  // a thread's tokens c4 * 2, c4 * 2 + 1 (and 8 more on) of a row of sums
+  const float* xsums = (const float*)xbase + c4 * 4;
+  auto two_tokens = [](float2 (&v)[NT], const float* p, int stage_at) {
+    p = (const float*)((const uint8_t*)p + stage_at);
+    if constexpr (NT == 2) {
+      const float4 u = *(const float4*)p;
+      v[0] = make_float2(u.x, u.y), v[1] = make_float2(u.z, u.w);
+    } else {
+      v[0] = *(const float2*)p;
+    }
+  };
   const uint32_t crow = cring + (lane & 15) * 128;
   const uint8_t* xrow[NT];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) xrow[n] = xbase + min(n * 8 + g, nt - 1) * kXPitch + c4 * 16;
+  for (int n = 0; n < NT; ++n) xrow[n] = xbase + (min(n * 8 + g, nt - 1) + 1) * kXPitch + c4 * 16;
 #pragma unroll 1
   for (int kc = first; kc < chunks; kc += step) {
     cp_async_wait<S - 1>();
@@ -314,29 +334,27 @@ __global__ void __launch_bounds__(256, Shape<NT, WR>::PER_SM) k_w4(W4Args a) {
     fetch_scales(kc + step);
     const uint32_t cb = crow + stage * STAGE;
     const int blocks = min(8, a.K / 32 - kc * 8);  // of 32 values, in this chunk
-    float back[NT][2], chunk[NT][4] = {};  // chunk: its sums, scaled by the groups' scales
+    float2 back[NT], chunk[NT][2] = {};  // chunk: its sums, scaled by the groups' scales
     if constexpr (PREP) {
       uint8_t* xc = xbase + stage * xstage;
       if constexpr (!PRE) {
 #pragma unroll 1
         for (int t = wr; t < nt; t += WR) {
-          uint8_t* p = xc + t * kXPitch;
-          prepare_chunk<DT, FMT>(*(const uint4*)(p + lane * 16), G32, p, lane);
+          const uint8_t* p = xc + (t + 1) * kXPitch;
+          prepare_chunk<DT, FMT>(*(const uint4*)(p + lane * 16), G32, xc, t, lane);
         }
         group_sync();
       }
+      two_tokens(back, xsums + kUndo, stage * xstage);
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-          back[n][q] = *(const float*)(xc + min(n * 8 + c4 * 2 + q, nt - 1) * kXPitch + kUndo) *
-                       (U4 ? 16777216.f : 1.f);  // u4 sums are in units of 2^-24
+      for (int n = 0; n < NT; ++n)  // u4 sums are in units of 2^-24
+        if (U4) back[n] = mul2(back[n], make_float2(16777216.f, 16777216.f));
     }
     // G32 == 0: the scale group, and what is left of it in blocks
     int grp = G32 ? 0 : kc * 8 / a.g32;
     int left = G32 ? 0 : (grp + 1) * a.g32 - kc * 8;
     uint32_t s[2];
-    float sx[NT][2];
+    float2 sx[NT];
     auto begin_group = [&](int local) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -348,7 +366,7 @@ __global__ void __launch_bounds__(256, Shape<NT, WR>::PER_SM) k_w4(W4Args a) {
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) sum[n][q] = 0.f;
-          sx[n][0] = sx[n][1] = 0.f;
+          sx[n] = make_float2(0.f, 0.f);
         }
       }
     };
@@ -370,15 +388,10 @@ __global__ void __launch_bounds__(256, Shape<NT, WR>::PER_SM) k_w4(W4Args a) {
       const bool end = G32 ? (j + 1) % (G32 ? G32 : 1) == 0 : --left == 0 || last;
       if constexpr (U4) {
         if (G32 == 0 || end) {
+          float2 v[NT];
+          two_tokens(v, xsums + (G32 ? j / (G32 ? G32 : 1) : j) * kTokens, stage * xstage);
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              const float v = *(const float*)(xbase + stage * xstage +
-                                              min(n * 8 + c4 * 2 + q, nt - 1) * kXPitch + kSums +
-                                              (G32 ? j / (G32 ? G32 : 1) : j) * 4);
-              sx[n][q] = G32 ? v : sx[n][q] + v;
-            }
+          for (int n = 0; n < NT; ++n) sx[n] = G32 ? v[n] : add2(sx[n], v[n]);
         }
       }
       if (end) {
@@ -389,14 +402,12 @@ __global__ void __launch_bounds__(256, Shape<NT, WR>::PER_SM) k_w4(W4Args a) {
           // 2^23 + zero, less 2^23
           const float zero = U4 ? __uint_as_float(0x4b000000u | (s[h] & 0xffu)) - 8388608.f : 0.f;
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              float v = sum[n][2 * h + q];
-              if constexpr (U4) v = fmaf(-zero, sx[n][q], v);
-              if constexpr (PREP) chunk[n][2 * h + q] = fmaf(f, v, chunk[n][2 * h + q]);
-              else acc[n][2 * h + q] = fmaf(f, v, acc[n][2 * h + q]);
-            }
+          for (int n = 0; n < NT; ++n) {
+            float2 v = make_float2(sum[n][2 * h], sum[n][2 * h + 1]);
+            if constexpr (U4) v = fma2(make_float2(-zero, -zero), sx[n], v);
+            float2& to = PREP ? chunk[n][h] : acc[n][h];
+            to = fma2(make_float2(f, f), v, to);
+          }
         }
         if (!last) {
           if (!G32) ++grp, left = a.g32;
@@ -438,7 +449,7 @@ __global__ void __launch_bounds__(256, Shape<NT, WR>::PER_SM) k_w4(W4Args a) {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) acc[n][q] = fmaf(back[n][q & 1], chunk[n][q], acc[n][q]);
+        for (int h = 0; h < 2; ++h) acc[n][h] = fma2(back[n], chunk[n][h], acc[n][h]);
     }
     group_sync();
     issue_codes(kc + S * step, stage);
@@ -456,7 +467,10 @@ __global__ void __launch_bounds__(256, Shape<NT, WR>::PER_SM) k_w4(W4Args a) {
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) red[(w * NT + n) * 128 + q * 32 + lane] = acc[n][q];
+    for (int h = 0; h < 2; ++h) {
+      red[(w * NT + n) * 128 + h * 64 + lane] = acc[n][h].x;
+      red[(w * NT + n) * 128 + h * 64 + 32 + lane] = acc[n][h].y;
+    }
   __syncthreads();
   if (csize > 1) {
     if (a.wk > 1) {
@@ -529,7 +543,7 @@ moe_status launch_w4(W4Args a, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(tiles * cluster, passes);
   cfg.blockDim = dim3(a.wk * WR * 32);
-  cfg.dynamicSmemBytes = (size_t)a.wk * Shape<NT, WR>::S * (ROWS * (kChunk / 2) + nt * kXPitch);
+  cfg.dynamicSmemBytes = (size_t)a.wk * Shape<NT, WR>::S * (ROWS * (kChunk / 2) + (nt + 1) * kXPitch);
   cfg.stream = s;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
