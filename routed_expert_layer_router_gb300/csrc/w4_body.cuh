@@ -24,7 +24,7 @@ namespace moe {
 
 struct W4Args {
   int T, N, K, G, g32, zrow;           // G groups of 32 * g32 values; zero bytes a row
-  int wk;                              // warps along K in a CTA
+  int wr_log, wk;                      // warps of a CTA: 2^wr_log along the rows, wk along K
   const uint16_t* x;
   const uint8_t* codes;
   const uint16_t* scales;
@@ -39,6 +39,7 @@ namespace {
 
 constexpr int kChunk = 256;            // input values of a stage: 128 bytes of a row
 constexpr int kMostCtas = 8;           // of a cluster
+constexpr int kMostSmem = 224 * 1024, kSmSmem = 228 * 1024;  // of a CTA, of an SM
 constexpr int kTokens = 16;            // tokens of one pass over the weights
 // A chunk of x, in shared memory and in the workspace: a row of group sums and of
 // what undoes each token's power of two, then a row for each token's 256 values
@@ -157,15 +158,12 @@ __device__ __forceinline__ float cluster_load(uint32_t addr, uint32_t rank) {
 }
 
 // Stages of a ring, and how many CTAs the GPU is given at once
-template <int NT, int WR>
+template <int NT>
 struct Shape {
   static constexpr int S = NT == 2 ? 4 : 3;
-  static constexpr int PER_SM = NT == 2 ? 2 : 3, CTAS = PER_SM * kSMs;
+  static constexpr int PER_SM = NT == 2 ? 2 : 3;
 };
 
-// NT: token tiles of 8.  WR: warps along the rows of W,
-// which share x.  G32: the group's length in blocks of 32 values where it is 1, 2 or 4,
-// so that its ends are known at compile time and its scales come a chunk ahead; 0: any.
 // x of many tokens, prepared once for all CTAs: a warp a token's chunk
 template <int DT, int FMT>
 __global__ void __launch_bounds__(128) k_w4_prepare(W4Args a) {
@@ -181,20 +179,27 @@ __global__ void __launch_bounds__(128) k_w4_prepare(W4Args a) {
   prepare_chunk<DT, FMT>(v, a.g32, to, t % kTokens, lane);
 }
 
-// PRE: x comes prepared from the workspace; the kernel that prepares it is the one
-// before, and all before that one are done when this one starts, so the codes'
-// loads need not wait for it.
-template <int DT, int FMT, int NT, int WR, int G32, bool PRE>
-__global__ void __launch_bounds__(256, Shape<NT, WR>::PER_SM) k_w4(W4Args a) {
+// NT: token tiles of 8.  G32: the group's length in blocks of 32 values where it is 1,
+// 2 or 4, so that its ends are known at compile time and its scales come a chunk
+// ahead; 0: any.
+// FIX: 0, or warps along the rows that are known at compile time: 1, one token, or 8
+// with PRE (13 x 9216 x 6144: 12.9 us, 14.9 as one kernel with the others; 1 x 6144 x
+// 6144: 7.7 and 8.0).
+// PRE: x comes prepared from the workspace.  The kernel that prepares it is the one
+// before, and all before that one are done when this one starts, so the codes' and
+// scales' loads need not wait for it.
+template <int DT, int FMT, int NT, int G32, int FIX, bool PRE>
+__global__ void __launch_bounds__(256, Shape<NT>::PER_SM) k_w4(W4Args a) {
   constexpr bool PREP = kPrepares<DT, FMT>, U4 = FMT == MOE_W4_U4;
-  constexpr int S = Shape<NT, WR>::S;          // all under way; a stage is refilled once used
+  constexpr int S = Shape<NT>::S;          // all under way; a stage is refilled once used
   constexpr int ROWS = 16;                  // of a warp
   constexpr int STAGE = ROWS * kChunk / 2;  // bytes of one warp's stage of codes
   constexpr int NG = G32 ? 8 / G32 : 1;     // groups of a chunk
   constexpr int SV = NG == 8 ? 2 : 1;       // of which a lane fetches this many
   extern __shared__ __align__(128) uint8_t sm[];
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int wr = w % WR, kw = w / WR;       // place along rows, along K
+  const int WR = FIX ? FIX : 1 << a.wr_log;
+  const int wr = w & (WR - 1), kw = FIX == 1 ? w : FIX == 8 ? 0 : w >> a.wr_log;  // along rows, K
   const int g = lane >> 2, c4 = lane & 3;
   const int crank = cluster_rank(), csize = cluster_size();
   const int n0 = ((blockIdx.x / csize) * WR + wr) * ROWS, t0 = blockIdx.y * kTokens;
@@ -304,8 +309,8 @@ __global__ void __launch_bounds__(256, Shape<NT, WR>::PER_SM) k_w4(W4Args a) {
   float sum[NT][4];
   int stage = 0;
   auto group_sync = [&]() {  // the warps that share a chunk
-    if constexpr (WR == 1) __syncwarp();
-    else asm volatile("bar.sync %0, %1;" ::"r"(1 + kw), "n"(WR * 32) : "memory");
+    if (WR == 1) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(1 + kw), "r"(WR * 32) : "memory");
   };
   // a thread's tokens c4 * 2, c4 * 2 + 1 (and 8 more on) of a row of sums
   const float* xsums = (const float*)xbase + c4 * 4;
@@ -462,7 +467,7 @@ __global__ void __launch_bounds__(256, Shape<NT, WR>::PER_SM) k_w4(W4Args a) {
 
   // sums over the warps along K in their order, then over the cluster in rank
   // order; the outputs are dealt to its CTAs
-  constexpr int OUT = WR * NT * 128;
+  const int OUT = WR * NT * 128;
   float* red = (float*)sm;
 #pragma unroll
   for (int n = 0; n < NT; ++n)
@@ -507,43 +512,23 @@ __global__ void __launch_bounds__(256, Shape<NT, WR>::PER_SM) k_w4(W4Args a) {
   if (csize > 1) cluster_sync();  // until all have read
 }
 
-template <int DT, int FMT, int NT, int WR, int G32>
-moe_status launch_w4(W4Args a, cudaStream_t s) {
-  // more than 8 tokens: prepared by a kernel of its own
-  constexpr bool PRE = NT == 2 && kPrepares<DT, FMT>;
-  auto* kern = k_w4<DT, FMT, NT, WR, G32, PRE>;
+template <int DT, int FMT, int NT, int G32, int FIX, bool PRE>
+moe_status launch_w4(const W4Args& a, dim3 grid, int cluster, int smem, cudaStream_t s) {
+  auto* kern = k_w4<DT, FMT, NT, G32, FIX, PRE>;
   static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is raised
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return launch_status(cudaErrorUnknown);
   const uint64_t bit = 1ull << (dev & 63);
   if (!(ready.load(std::memory_order_relaxed) & bit)) {
     const cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
     if (e != cudaSuccess) return launch_status(e);
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
-  constexpr int ROWS = 16 * WR;
-  const int chunks = (a.K + kChunk - 1) / kChunk;
-  const int tiles = (a.N + ROWS - 1) / ROWS, passes = (a.T + kTokens - 1) / kTokens;
-  const int nt = a.T < NT * 8 ? a.T : NT * 8;
-  // 8 warps a CTA, then as large a cluster along K as the GPU holds at once, but
-  // no larger than shortens the longest share of the chunks; of two CTAs an SM, 6
-  // do not pack (16 tokens, 6144 x 6144: 18 us in clusters of 6, 13.5 in fours)
-  a.wk = 8 / WR < chunks ? 8 / WR : chunks;
-  auto share = [&](int c) { return (chunks + a.wk * c - 1) / (a.wk * c); };
-  int cluster = kMostCtas;
-  while (cluster > 1 && ((int64_t)tiles * passes * cluster > Shape<NT, WR>::CTAS ||
-                         share(cluster) == share(cluster - 1) ||
-                         (NT == 2 && (cluster & (cluster - 1)))))
-    --cluster;
-  if constexpr (PRE) {
-    const cudaError_t e = launch_pdl(k_w4_prepare<DT, FMT>, dim3(chunks, (a.T + 3) / 4), 128, 0, s, a);
-    if (e != cudaSuccess) return launch_status(e);
-  }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(tiles * cluster, passes);
-  cfg.blockDim = dim3(a.wk * WR * 32);
-  cfg.dynamicSmemBytes = (size_t)a.wk * Shape<NT, WR>::S * (ROWS * (kChunk / 2) + (nt + 1) * kXPitch);
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(a.wk * (32 << a.wr_log));
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -556,20 +541,71 @@ moe_status launch_w4(W4Args a, cudaStream_t s) {
   return launch_status(cudaLaunchKernelEx(&cfg, kern, a));
 }
 
-template <int DT, int FMT, int NT, int WR>
-moe_status pick_group(const W4Args& a, cudaStream_t s) {
-  if (a.g32 == 1) return launch_w4<DT, FMT, NT, WR, 1>(a, s);
-  if (a.g32 == 2) return launch_w4<DT, FMT, NT, WR, 2>(a, s);
-  if (a.g32 == 4) return launch_w4<DT, FMT, NT, WR, 4>(a, s);
-  return launch_w4<DT, FMT, NT, WR, 0>(a, s);
+template <int DT, int FMT, int NT, int G32>
+moe_status shape_w4(W4Args a, cudaStream_t s) {
+  // How 8 warps are split into those along the rows (wr, which share x) and along K,
+  // and K over a cluster: what counts is a warp's share of the chunks.  The cost in
+  // units of about 0.14 us, from measurements: 6 a chunk, 1 a token that a warp
+  // prepares for it, 2 and 1 a CTA for a cluster's sum; times the waves of CTAs.
+  // (4 x 512 x 8192: wr 8 to 1: 6.4, 4.7, 4.2, 3.9 us; 4 x 8192 x 6144: 11.6, 12.1,
+  // 12.6, 22.3; 13 x 512 x 8192: 8.0, 6.1, 9.5 with 2; 1 x 6144 x 6144: 8.8, 9.2, 9.1,
+  // 8.0.)  Two CTAs an SM of clusters of 6 do not pack (16 tokens, 6144 x 6144: 18 us,
+  // 13.5 in fours).
+  const int chunks = (a.K + kChunk - 1) / kChunk;
+  const int passes = (a.T + kTokens - 1) / kTokens;
+  const int nt = a.T < NT * 8 ? a.T : NT * 8;
+  int tiles = 0, cluster = 1, smem = 0, share = 0, least = 0;
+  for (int wr_log = 3; wr_log >= 0; --wr_log) {
+    const int wr = 1 << wr_log, wk = 8 / wr < chunks ? 8 / wr : chunks;
+    const int bytes = wk * Shape<NT>::S * (((16 * kChunk / 2) << wr_log) + (nt + 1) * kXPitch);
+    if (bytes > kMostSmem) break;
+    const int fit = kSmSmem / (bytes + 1024), per_sm = fit < Shape<NT>::PER_SM ? fit : Shape<NT>::PER_SM;
+    const int n = (a.N + 16 * wr - 1) / (16 * wr);
+    const int64_t ctas = (int64_t)n * passes;
+    auto shared_by = [&](int c) { return (chunks + wk * c - 1) / (wk * c); };
+    int c = kMostCtas;
+    // a whole GPU of large clusters with an SM for each CTA does not pack either
+    while (c > 1 && (ctas * c > per_sm * kSMs * (per_sm == 1 && c > 4 ? 0.75f : 1.f) ||
+                     shared_by(c) == shared_by(c - 1) || (NT == 2 && (c & (c - 1)))))
+      --c;
+    const int64_t waves = (ctas * c + per_sm * kSMs - 1) / (per_sm * kSMs);
+    const int64_t cost = waves * shared_by(c) * (6 + (nt + wr - 1) / wr) + (c > 1 ? 2 + c : 0);
+    const int capped = cost < (1 << 30) ? (int)cost : 1 << 30;
+    if (wr_log == 3 || capped < least || (a.T == 1 && capped == least)) {
+      least = capped, share = shared_by(c), tiles = n, cluster = c, smem = bytes;
+      a.wr_log = wr_log, a.wk = wk;
+    }
+  }
+  // x of more than 8 tokens prepared by a kernel before costs a launch (1 us) and saves
+  // each of the 8 warps two tokens a chunk: from 4 chunks a warp on (13 tokens, groups
+  // of 64: 16384 x 2048 12.7 -> 11.6 us, 8192 x 6144 17.1 -> 14.9; at 2 chunks, 4096 x
+  // 4096, 7.5 -> 7.7)
+  const dim3 grid(tiles * cluster, passes);
+  if constexpr (kPrepares<DT, FMT> && NT == 2) {
+    if (a.wr_log == 3 && share >= 4) {
+      const cudaError_t e = launch_pdl(k_w4_prepare<DT, FMT>, dim3(chunks, (a.T + 3) / 4), 128, 0, s, a);
+      if (e != cudaSuccess) return launch_status(e);
+      return launch_w4<DT, FMT, NT, G32, 8, true>(a, grid, cluster, smem, s);
+    }
+  }
+  if constexpr (NT == 1) {
+    if (a.T == 1 && a.wr_log == 0)
+      return launch_w4<DT, FMT, NT, G32, 1, false>(a, grid, cluster, smem, s);
+  }
+  return launch_w4<DT, FMT, NT, G32, 0, false>(a, grid, cluster, smem, s);
 }
 
-// One token: each warp keeps its own x (no barrier between warps).  Up to 8 are
-// prepared by the CTA for its 8 warps of different rows; more by a kernel before.
+template <int DT, int FMT, int NT>
+moe_status pick_group(const W4Args& a, cudaStream_t s) {
+  if (a.g32 == 1) return shape_w4<DT, FMT, NT, 1>(a, s);
+  if (a.g32 == 2) return shape_w4<DT, FMT, NT, 2>(a, s);
+  if (a.g32 == 4) return shape_w4<DT, FMT, NT, 4>(a, s);
+  return shape_w4<DT, FMT, NT, 0>(a, s);
+}
+
 template <int DT, int FMT>
 moe_status pick_w4(const W4Args& a, cudaStream_t s) {
-  if (a.T == 1) return pick_group<DT, FMT, 1, 1>(a, s);
-  return a.T <= 8 ? pick_group<DT, FMT, 1, 8>(a, s) : pick_group<DT, FMT, 2, 8>(a, s);
+  return a.T <= 8 ? pick_group<DT, FMT, 1>(a, s) : pick_group<DT, FMT, 2>(a, s);
 }
 
 }  // namespace
