@@ -551,10 +551,16 @@ moe_status shape_w4(W4Args a, cudaStream_t s) {
   // 12.6, 22.3; 13 x 512 x 8192: 8.0, 6.1, 9.5 with 2; 1 x 6144 x 6144: 8.8, 9.2, 9.1,
   // 8.0.)  Two CTAs an SM of clusters of 6 do not pack (16 tokens, 6144 x 6144: 18 us,
   // 13.5 in fours).
+  // x of more than 8 tokens prepared by a kernel before costs a launch, and saves each of
+  // the 8 warps that share it two tokens a chunk: from two chunks a warp on (16 tokens,
+  // groups of 128, 8192 x 4096: 11.3 -> 9.7 us; 13, groups of 64, 4096 x 4096: 7.2 ->
+  // 7.0).
   const int chunks = (a.K + kChunk - 1) / kChunk;
   const int passes = (a.T + kTokens - 1) / kTokens;
   const int nt = a.T < NT * 8 ? a.T : NT * 8;
-  int tiles = 0, cluster = 1, smem = 0, share = 0, least = 0;
+  constexpr bool prepares = kPrepares<DT, FMT> && NT == 2;
+  bool before = false;
+  int tiles = 0, cluster = 1, smem = 0, least = 0;
   for (int wr_log = 3; wr_log >= 0; --wr_log) {
     const int wr = 1 << wr_log, wk = 8 / wr < chunks ? 8 / wr : chunks;
     const int bytes = wk * Shape<NT>::S * (((16 * kChunk / 2) << wr_log) + (nt + 1) * kXPitch);
@@ -569,20 +575,18 @@ moe_status shape_w4(W4Args a, cudaStream_t s) {
                      shared_by(c) == shared_by(c - 1) || (NT == 2 && (c & (c - 1)))))
       --c;
     const int64_t waves = (ctas * c + per_sm * kSMs - 1) / (per_sm * kSMs);
-    const int64_t cost = waves * shared_by(c) * (6 + (nt + wr - 1) / wr) + (c > 1 ? 2 + c : 0);
+    const bool pre = prepares && wr == 8 && shared_by(c) >= 2;
+    const int64_t cost = waves * shared_by(c) * (6 + (pre ? 0 : (nt + wr - 1) / wr)) +
+                         (pre ? 4 : 0) + (c > 1 ? 2 + c : 0);
     const int capped = cost < (1 << 30) ? (int)cost : 1 << 30;
-    if (wr_log == 3 || capped < least || (a.T == 1 && capped == least)) {
-      least = capped, share = shared_by(c), tiles = n, cluster = c, smem = bytes;
+    if (wr_log == 3 || capped < least || (NT == 1 && capped == least)) {
+      least = capped, before = pre, tiles = n, cluster = c, smem = bytes;
       a.wr_log = wr_log, a.wk = wk;
     }
   }
-  // x of more than 8 tokens prepared by a kernel before costs a launch (1 us) and saves
-  // each of the 8 warps two tokens a chunk: from 4 chunks a warp on (13 tokens, groups
-  // of 64: 16384 x 2048 12.7 -> 11.6 us, 8192 x 6144 17.1 -> 14.9; at 2 chunks, 4096 x
-  // 4096, 7.5 -> 7.7)
   const dim3 grid(tiles * cluster, passes);
-  if constexpr (kPrepares<DT, FMT> && NT == 2) {
-    if (a.wr_log == 3 && share >= 4) {
+  if constexpr (prepares) {
+    if (before) {
       const cudaError_t e = launch_pdl(k_w4_prepare<DT, FMT>, dim3(chunks, (a.T + 3) / 4), 128, 0, s, a);
       if (e != cudaSuccess) return launch_status(e);
       return launch_w4<DT, FMT, NT, G32, 8, true>(a, grid, cluster, smem, s);
