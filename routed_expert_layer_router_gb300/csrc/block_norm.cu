@@ -208,15 +208,39 @@ __device__ __forceinline__ float2 block_sum2(float2 v, float (*part)[64], int& s
 // rows at a time halve the barriers, and packed fp32 the arithmetic.
 // The 8 values are 8 in a row where all are 16 bits wide, else 4 and 4 (half a
 // row apart), so that a warp's fp32 accesses are whole runs of 512 bytes.
-template <int RT, int BT, int MAXT>
+//
+// ODD: rows that begin anywhere (an odd H), all tensors' alike.  A thread's 8 values (or
+// 4 and 4) are counted from the aligned place at or before the row's begin, so copies
+// and stores stay whole; what they hold of the rows on both sides is masked out, and is
+// neither read past the row's end nor written.  A CTA's rows are a multiple of 8 apart,
+// so they all begin alike, and the weights stay in registers here too.
+template <int RT, int BT, int MAXT, bool ODD>
 __global__ void __launch_bounds__(MAXT) k_block_norm_rows(NormArgs a, int stages) {
   constexpr bool SPLIT = RT == MOE_DT_F32;
+  constexpr int RUN = SPLIT ? 4 : 8;  // values of an aligned access
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float part[2][64];
   int slot = 0;
   const int tid = threadIdx.x, nthr = blockDim.x;
   const int o0 = SPLIT ? tid * 4 : tid * 8, o1 = SPLIT ? (tid + nthr) * 4 : tid * 8 + 4;
-  const bool in0 = o0 < a.H, in1 = o1 < a.H;
+  const bool in0 = o0 < a.H, in1 = o1 < a.H;  // !ODD
+  // ODD: values before a row in its first access, and what of 4 values at o lies in it
+  const int off = ODD ? (int)(blockIdx.x * a.ldx) & (RUN - 1) : 0;
+  auto inside = [&](int o, float2& u, float2& v) {
+    const int p = o - off;
+    if (p < 0 || p + 4 > a.H) {
+      if (p < 0 || p >= a.H) u.x = 0.f;
+      if (p + 1 < 0 || p + 1 >= a.H) u.y = 0.f;
+      if (p + 2 < 0 || p + 2 >= a.H) v.x = 0.f;
+      if (p + 3 < 0 || p + 3 >= a.H) v.y = 0.f;
+    }
+  };
+  auto mask = [&](float2 (&v)[2][4]) {
+    if constexpr (ODD) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) inside(o0, v[q][0], v[q][1]), inside(o1, v[q][2], v[q][3]);
+    }
+  };
   const bool full_gate = a.gate && a.gate_col && a.gate_row;
   constexpr int XB = RT == MOE_DT_F32 ? 32 : 16, BB = BT == MOE_DT_F32 ? 32 : 16;  // of a thread
   const int row_bytes = (XB + (a.y ? BB : 0) + (full_gate ? BB : 0)) * nthr;
@@ -227,13 +251,25 @@ __global__ void __launch_bounds__(MAXT) k_block_norm_rows(NormArgs a, int stages
   // a row's share of this thread, as it lies in the ring
   auto copy = [&](auto dt, const void* p, uint32_t d) {
     constexpr int DT = decltype(dt)::value;
-    const typename Elem<DT>::T* q = (const typename Elem<DT>::T*)p;
-    if constexpr (DT == MOE_DT_F32) {
+    const typename Elem<DT>::T* q = (const typename Elem<DT>::T*)p - off;
+    if constexpr (ODD) {
+      constexpr int ES = DT == MOE_DT_F32 ? 4 : 2;
+      const int n0 = min(a.H + off - o0, RUN), n1 = min(a.H + off - o1, RUN);
+      if constexpr (DT == MOE_DT_F32) {
+        if (n0 > 0) cp_async16(d + tid * 16, q + o0, n0 * ES);
+        if (n1 > 0) cp_async16(d + (tid + nthr) * 16, q + o1, n1 * ES);
+      } else if constexpr (SPLIT) {
+        if (n0 > 0) cp_async8(d + tid * 8, q + o0, n0 * ES);
+        if (n1 > 0) cp_async8(d + (tid + nthr) * 8, q + o1, n1 * ES);
+      } else {
+        if (n0 > 0) cp_async16(d + tid * 16, q + o0, n0 * ES);
+      }
+    } else if constexpr (DT == MOE_DT_F32) {
       if (in0) cp_async16(d + tid * 16, q + o0, 16);
       if (in1) cp_async16(d + (tid + nthr) * 16, q + o1, 16);
     } else if constexpr (SPLIT) {
-      if (in0) cp_async8(d + tid * 8, q + o0);
-      if (in1) cp_async8(d + (tid + nthr) * 8, q + o1);
+      if (in0) cp_async8(d + tid * 8, q + o0, 8);
+      if (in1) cp_async8(d + (tid + nthr) * 8, q + o1, 8);
     } else {
       if (in0) cp_async16(d + tid * 16, q + o0, 16);
     }
@@ -261,8 +297,15 @@ __global__ void __launch_bounds__(MAXT) k_block_norm_rows(NormArgs a, int stages
   // straight from and to global memory, at o0 and o1
   auto load_at = [&](auto dt, const void* p, float2 (&v)[4]) {
     constexpr int DT = decltype(dt)::value;
-    const typename Elem<DT>::T* q = (const typename Elem<DT>::T*)p;
-    if constexpr (DT == MOE_DT_F32) {
+    const typename Elem<DT>::T* q = (const typename Elem<DT>::T*)p - off;
+    if constexpr (ODD) {
+      auto one = [&](int o) { return o >= off && o < a.H + off ? to_f32<DT>(q[o]) : 0.f; };
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        v[j] = make_float2(one(o0 + 2 * j), one(o0 + 2 * j + 1));
+        v[2 + j] = make_float2(one(o1 + 2 * j), one(o1 + 2 * j + 1));
+      }
+    } else if constexpr (DT == MOE_DT_F32) {
       const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
       const float4 x = in0 ? *(const float4*)(q + o0) : z, y = in1 ? *(const float4*)(q + o1) : z;
       v[0] = make_float2(x.x, x.y), v[1] = make_float2(x.z, x.w);
@@ -275,7 +318,18 @@ __global__ void __launch_bounds__(MAXT) k_block_norm_rows(NormArgs a, int stages
   };
   auto put = [&](auto dt, void* p, const float2 (&v)[4]) {
     constexpr int DT = decltype(dt)::value;
-    typename Elem<DT>::T* q = (typename Elem<DT>::T*)p;
+    typename Elem<DT>::T* q = (typename Elem<DT>::T*)p - off;
+    bool in0 = o0 < a.H, in1 = o1 < a.H;
+    if constexpr (ODD) {
+      const int p0 = o0 - off, p1 = o1 - off;
+      in0 = p0 >= 0 && p0 + RUN <= a.H, in1 = SPLIT && p1 >= 0 && p1 + RUN <= a.H;
+      auto edge = [&](int o, const float2& x) {
+        if (o >= off && o < a.H + off) q[o] = from_f32<DT>(x.x);
+        if (o + 1 >= off && o + 1 < a.H + off) q[o + 1] = from_f32<DT>(x.y);
+      };
+      if (!in0) edge(o0, v[0]), edge(o0 + 2, v[1]);
+      if (SPLIT ? !in1 : !in0) edge(o1, v[2]), edge(o1 + 2, v[3]);
+    }
     if constexpr (DT == MOE_DT_F32) {
       if (in0) *(float4*)(q + o0) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
       if (in1) *(float4*)(q + o1) = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
@@ -297,11 +351,13 @@ __global__ void __launch_bounds__(MAXT) k_block_norm_rows(NormArgs a, int stages
   using BE = typename Elem<BT>::T;
 
   const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
-  const int64_t pairs = ((int64_t)a.T + 1) / 2;
-  auto issue = [&](int64_t pair, int stage) {
+  // rows of a pair, and from a pair to the next: neighbours, or grid rows apart
+  const int64_t mate = ODD ? gridDim.x : 1, step = 2 * gridDim.x;
+  const int64_t t0 = ODD ? blockIdx.x : 2 * blockIdx.x;
+  auto issue = [&](int64_t first, int stage) {
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      const int64_t t = 2 * pair + q;
+      const int64_t t = first + q * mate;
       if (t < a.T) {
         uint32_t d = ring_at + (stage * 2 + q) * row_bytes;
         copy(rt, (const RE*)a.x + t * a.ldx, d);
@@ -311,8 +367,7 @@ __global__ void __launch_bounds__(MAXT) k_block_norm_rows(NormArgs a, int stages
     }
     cp_async_commit();
   };
-  const int64_t step = gridDim.x;
-  for (int k = 0; k < stages - 1; ++k) issue(blockIdx.x + k * step, k);
+  for (int k = 0; k < stages - 1; ++k) issue(t0 + k * step, k);
 
   float2 w_post[4], w_pre[4], cg[4];
   auto vector = [&](const void* w, float2 (&v)[4]) {
@@ -343,6 +398,7 @@ __global__ void __launch_bounds__(MAXT) k_block_norm_rows(NormArgs a, int stages
 
   // sum of this thread's terms of a row; what lies outside it counts nothing
   auto own = [&](const float2& u, const float2& v) {
+    if constexpr (ODD) return (u.x + u.y) + (v.x + v.y);
     return (in0 ? u.x + u.y : 0.f) + (in1 ? v.x + v.y : 0.f);
   };
   auto norm = [&](float2 (&v)[2][4], const float2 (&w)[4], const void* c) {
@@ -356,6 +412,7 @@ __global__ void __launch_bounds__(MAXT) k_block_norm_rows(NormArgs a, int stages
       for (int q = 0; q < 2; ++q)
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[q][j] = add2(v[q][j], make_float2(m[q], m[q]));
+      mask(v);
     }
     float s[2];
 #pragma unroll
@@ -379,13 +436,12 @@ __global__ void __launch_bounds__(MAXT) k_block_norm_rows(NormArgs a, int stages
   };
 
   int stage = 0;
-  for (int64_t pair = blockIdx.x; pair < pairs; pair += step) {
+  for (int64_t t = t0; t < a.T; t += step) {
     // the oldest group is this pair's; an empty group keeps the count at the end
     if (stages == 2) cp_async_wait<0>();
     else if (stages == 3) cp_async_wait<1>();
     else cp_async_wait<2>();
-    const int64_t t = 2 * pair;
-    const bool two = t + 1 < a.T;
+    const bool two = t + mate < a.T;
     float2 r[2][4] = {}, b[2][4] = {};
     const uint8_t* row = ring + stage * 2 * row_bytes;
 #pragma unroll
@@ -395,7 +451,12 @@ __global__ void __launch_bounds__(MAXT) k_block_norm_rows(NormArgs a, int stages
         if (a.y) take(bt, row + q * row_bytes + XB * nthr, b[q]);
       }
     }
-    if (a.post_norm) norm(b, w_post, a.b_post);
+    mask(r);
+    mask(b);
+    if (a.post_norm) {
+      norm(b, w_post, a.b_post);
+      mask(b);  // an infinite sum, a bias
+    }
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       if (q == 1 && !two) continue;
@@ -406,7 +467,7 @@ __global__ void __launch_bounds__(MAXT) k_block_norm_rows(NormArgs a, int stages
         for (int j = 0; j < 4; ++j) g[j] = make_float2(gated(g[j].x), gated(g[j].y));
       } else if (a.gate && !a.gate_col) {
         float one[1];
-        load<BT, 1>(a.gate, (t + q) * a.gate_row, one);
+        load<BT, 1>(a.gate, (t + q * mate) * a.gate_row, one);
         one[0] = gated(one[0]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) g[j] = make_float2(one[0], one[0]);
@@ -417,36 +478,41 @@ __global__ void __launch_bounds__(MAXT) k_block_norm_rows(NormArgs a, int stages
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         r[q][j] = fma2(r[q][j], make_float2(a.res_scale, a.res_scale), mul2(b[q][j], g[j]));
-      if (a.r) put(rt, (RE*)a.r + (t + q) * a.ldr, r[q]);
+      if (ODD) inside(o0, r[q][0], r[q][1]), inside(o1, r[q][2], r[q][3]);  // an infinite gate
+      if (a.r) put(rt, (RE*)a.r + (t + q * mate) * a.ldr, r[q]);
     }
     // this pair's stage has been read: the pair `stages - 1` ahead goes behind it
-    issue(pair + (stages - 1) * step, stage == 0 ? stages - 1 : stage - 1);
+    issue(t + (stages - 1) * step, stage == 0 ? stages - 1 : stage - 1);
     stage = stage + 1 == stages ? 0 : stage + 1;
     if (a.h) {
       norm(r, w_pre, a.b_pre);
 #pragma unroll
       for (int q = 0; q < 2; ++q)
-        if (q == 0 || two) put(bt, (BE*)a.h + (t + q) * a.ldh, r[q]);
+        if (q == 0 || two) put(bt, (BE*)a.h + (t + q * mate) * a.ldh, r[q]);
     }
   }
   cp_async_wait<0>();
 }
 
-template <int RT, int BT, int MAXT>
-cudaError_t launch_rows(const NormArgs& a, cudaStream_t s) {
-  auto* kern = k_block_norm_rows<RT, BT, MAXT>;
+// false where a row is too long for it
+template <int RT, int BT, int MAXT, bool ODD>
+bool launch_rows(const NormArgs& a, cudaStream_t s, cudaError_t& e) {
+  static_assert(kSMs % 8 == 0, "rows of a CTA");
+  auto* kern = k_block_norm_rows<RT, BT, MAXT, ODD>;
   static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is raised
   int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
+  e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return true;
   constexpr int kMost = 224 * 1024;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(ready.load(std::memory_order_relaxed) & bit)) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess) return true;
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
-  const int threads = ((a.H + 7) / 8 + 31) / 32 * 32;
+  // ODD: up to 7 values (3 where accesses are of 4) before a row
+  const int threads = ((a.H + (ODD ? 7 : 0) + 7) / 8 + 31) / 32 * 32;
+  if (threads > MAXT) return false;
   const int planes = (RT == MOE_DT_F32 ? 2 : 1) +
                      (BT == MOE_DT_F32 ? 2 : 1) *
                          ((a.y ? 1 : 0) + (a.gate && a.gate_col && a.gate_row ? 1 : 0));
@@ -459,8 +525,9 @@ cudaError_t launch_rows(const NormArgs& a, cudaStream_t s) {
   stages = stages > 4 ? 4 : stages < 2 ? 2 : stages;
   while (per_sm > 1 && per_sm * (stages * pair + 1536) > 227 * 1024) --per_sm;
   const int pairs = (a.T + 1) / 2;
-  const int grid = pairs < per_sm * kSMs ? pairs : per_sm * kSMs;
-  return launch_pdl(kern, grid, threads, (size_t)stages * pair, s, a, stages);
+  const int most = per_sm * kSMs, few = ODD ? (pairs + 7) / 8 * 8 : pairs;
+  e = launch_pdl(kern, few < most ? few : most, threads, (size_t)stages * pair, s, a, stages);
+  return true;
 }
 
 template <int RT, int BT, int VEC, int VPT, int MAXT>
@@ -472,14 +539,21 @@ cudaError_t launch(const NormArgs& a, cudaStream_t s) {
 // Few rows: one access a thread, so that a row's loads leave together (the
 // call's latency).  More than the GPU holds at once: the kernel that stays.
 template <int RT, int BT>
-cudaError_t dispatch(const NormArgs& a, int vec, cudaStream_t s) {
+cudaError_t dispatch(const NormArgs& a, int vec, bool alike, cudaStream_t s) {
   const int H = a.H;
   if (vec == 8) {
-    if (a.T > 2 * kSMs && H <= 8 * 1024)
-      return H <= 8 * 768 ? launch_rows<RT, BT, 768>(a, s) : launch_rows<RT, BT, 1024>(a, s);
+    cudaError_t e;
+    if (a.T > 2 * kSMs && H <= 8 * 1024 &&
+        (H <= 8 * 768 ? launch_rows<RT, BT, 768, false>(a, s, e)
+                      : launch_rows<RT, BT, 1024, false>(a, s, e)))
+      return e;
     if (H <= 8 * 1024) return launch<RT, BT, 8, 1, 1024>(a, s);
     if (H <= 8 * 2 * 1024) return launch<RT, BT, 8, 2, 1024>(a, s);
     return launch<RT, BT, 8, 4, 1024>(a, s);
+  }
+  if (a.T > 2 * kSMs && alike) {
+    cudaError_t e;
+    if (launch_rows<RT, BT, 768, true>(a, s, e) || launch_rows<RT, BT, 1024, true>(a, s, e)) return e;
   }
   if (vec == 2) {
     if (H <= 2 * 1024 && a.T <= 2 * kSMs) return launch<RT, BT, 2, 1, 1024>(a, s);
@@ -541,12 +615,19 @@ MOE_API moe_status moe_block_norm(const moe_block_norm_args* a, void* stream) {
            (!a->gate || a->gate_col == 0 || ok(a->gate, a->gate_row, BT));
   };
   const int vec = vec_ok(8) ? 8 : vec_ok(2) ? 2 : 1;
+  // rows of all tensors begin at the same place of an aligned run of 8 values
+  auto same = [&](const void* p, int64_t ld) {
+    return !p || ((uintptr_t)p % 16 == 0 && (ld - a->ldx) % 8 == 0);
+  };
+  const bool full_gate = a->gate && a->gate_col && a->gate_row;
+  const bool alike = same(a->x, a->ldx) && same(a->y, a->ldy) && same(a->r, a->ldr) &&
+                     same(a->h, a->ldh) && (!full_gate || same(a->gate, a->gate_row));
   cudaStream_t s = (cudaStream_t)stream;
   cudaError_t e;
-  if (RT == MOE_DT_BF16) e = dispatch<MOE_DT_BF16, MOE_DT_BF16>(k, vec, s);
-  else if (RT == MOE_DT_F16) e = dispatch<MOE_DT_F16, MOE_DT_F16>(k, vec, s);
-  else if (BT == MOE_DT_F32) e = dispatch<MOE_DT_F32, MOE_DT_F32>(k, vec, s);
-  else if (BT == MOE_DT_BF16) e = dispatch<MOE_DT_F32, MOE_DT_BF16>(k, vec, s);
-  else e = dispatch<MOE_DT_F32, MOE_DT_F16>(k, vec, s);
+  if (RT == MOE_DT_BF16) e = dispatch<MOE_DT_BF16, MOE_DT_BF16>(k, vec, alike, s);
+  else if (RT == MOE_DT_F16) e = dispatch<MOE_DT_F16, MOE_DT_F16>(k, vec, alike, s);
+  else if (BT == MOE_DT_F32) e = dispatch<MOE_DT_F32, MOE_DT_F32>(k, vec, alike, s);
+  else if (BT == MOE_DT_BF16) e = dispatch<MOE_DT_F32, MOE_DT_BF16>(k, vec, alike, s);
+  else e = dispatch<MOE_DT_F32, MOE_DT_F16>(k, vec, alike, s);
   return launch_status(e);
 }
