@@ -641,7 +641,8 @@ moe_status kvcache_append(const kvcache_append_args* a, void* stream);
  *   out = sum_n softmax(s)_n v_n,  lse = ln sum_n exp(s_n)   (fp32)
  * A row with no position to read (len 0, or none but bad pages) gives out 0
  * and lse -inf, as does a row whose every score is -inf.  Cache contents outside the
- * positions read never touch the result, NaN included.
+ * positions read never touch the result, NaN included; an infinite or NaN value of
+ * V that is read makes its column of the row NaN or infinite.
  *   - A page id outside [0, n_pages) leaves out that page's tokens, and a
  *     length outside [0, max_pages * page_size] is clamped to it; both set
  *     MOE_ERR_DEVICE in *status.
@@ -652,8 +653,9 @@ moe_status kvcache_append(const kvcache_append_args* a, void* stream);
  *     (every call leaves them zero).  Calls that share it must not overlap on
  *     the GPU.
  * Hq a multiple of Hkv; q and out 16-byte aligned with strides of a multiple of 8
- * elements; else MOE_ERR_UNSUPPORTED.  The pools' strides bound the call, not
- * the lengths. */
+ * elements; else MOE_ERR_UNSUPPORTED, as are 2^30 or more tiles of 64 tokens (B *
+ * Hkv * max_pages * page_size / 64, times the blocks of 8 query heads that share a
+ * kv head).  Offsets within the pools are 64 bits wide. */
 typedef struct {
   kvcache_view c;
   int B, Hq;
@@ -688,7 +690,7 @@ moe_status kvcache_attend(const kvcache_attend_args* a, void* stream);
  * that largest value; U4 zero points come off as sum code x - zero sum x.  An x
  * that is infinite or NaN makes its token's results NaN or infinite.
  * Meant for few tokens: the weights are read once for every 16 of them.  Calls that
- * share a workspace must not overlap on the GPU.
+ * share a workspace must not overlap on the GPU.  T <= 262140.
  * K a multiple of group, group a multiple of 32; codes and x 16-byte aligned,
  * ldx a multiple of 8; else MOE_ERR_UNSUPPORTED.  T == 0 is a no-op. */
 enum { MOE_W4_U4 = 0, MOE_W4_E2M1 = 1 };

@@ -2,10 +2,13 @@
 // the norms on both sides of it, the block's gate and the residual scale, in
 // one pass (formulas in moe.h).
 //
-// Bound by memory: x and y are read once, r and h written once.  A CTA owns a
-// row and keeps it in registers as fp32 (kVec * VPT values a thread), so the
-// statistics cost no second read; a layer norm's variance is taken around the
-// mean from the registers.  Weights and channel gates come through L1 / L2.
+// Bound by memory: x and y are read once, r and h written once.  A row stays in
+// registers as fp32 between its read and its write, so the statistics cost no
+// second read; a layer norm's variance is taken around the mean from the
+// registers.  Two kernels: a CTA a row where rows are few and the call's latency
+// counts (k_block_norm: one row of 6144 2.5 us; weights and channel gates come
+// through L1 / L2), and CTAs that walk many rows (k_block_norm_rows: 4096 rows of
+// 6144, fp32 stream, bf16 branch, norms on both sides: 54 us, 5.5 TB/s).
 #include <atomic>
 #include <type_traits>
 
@@ -71,6 +74,10 @@ __global__ void __launch_bounds__(MAXT) k_block_norm(NormArgs a) {
   pdl_wait();
   pdl_launch_dependents();
 
+  // access k of a row; one past its end reads the last again (what comes of it counts
+  // nothing), so that no load waits behind a branch
+  auto place = [&](int k) { return min(i0 + k * step, H - VEC); };
+
   // v <- N(v; w, c), rows' statistics over the CTA
   auto norm = [&](float (&v)[VPT][VEC], const void* w, const void* c) {
     float mean = 0.f;
@@ -93,67 +100,63 @@ __global__ void __launch_bounds__(MAXT) k_block_norm(NormArgs a) {
           s += v[k][j] * v[k][j];
         }
     const float rs = rsqrtf(block_sum(s, part, slot) * inv_h + a.eps);
+    auto with = [&](const void* p, auto op) {
+      auto all = [&](auto dt) {
 #pragma unroll
-    for (int k = 0; k < VPT; ++k) {
-      const int i = i0 + k * step;
-      if (i < H) {
-        float u[VEC];
-        if (w) {
-          if (a.w16) load<BT, VEC>(w, i, u);
-          else load<MOE_DT_F32, VEC>(w, i, u);
+        for (int k = 0; k < VPT; ++k) {
+          float u[VEC];
+          load<decltype(dt)::value, VEC>(p, place(k), u);
 #pragma unroll
-          for (int j = 0; j < VEC; ++j) v[k][j] *= rs * (u[j] + a.w_offset);
-        } else {
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) v[k][j] *= rs;
+          for (int j = 0; j < VEC; ++j) v[k][j] = op(v[k][j], u[j]);
         }
-        if (c) {
-          if (a.w16) load<BT, VEC>(c, i, u);
-          else load<MOE_DT_F32, VEC>(c, i, u);
+      };
+      if (a.w16) all(std::integral_constant<int, BT>());
+      else all(std::integral_constant<int, MOE_DT_F32>());
+    };
+    if (w) {
+      with(w, [&](float x, float u) { return x * (rs * (u + a.w_offset)); });
+    } else {
 #pragma unroll
-          for (int j = 0; j < VEC; ++j) v[k][j] += u[j];
-        }
-      }
+      for (int k = 0; k < VPT; ++k)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) v[k][j] *= rs;
     }
+    if (c) with(c, [](float x, float u) { return x + u; });
   };
 
   for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
     float r[VPT][VEC], b[VPT][VEC];
 #pragma unroll
-    for (int k = 0; k < VPT; ++k) {
-      const int i = i0 + k * step;
-      if (i < H) {
-        load<RT, VEC>(a.x, t * a.ldx + i, r[k]);
-        if (a.y) load<BT, VEC>(a.y, t * a.ldy + i, b[k]);
-      }
-    }
+    for (int k = 0; k < VPT; ++k) load<RT, VEC>(a.x, t * a.ldx + place(k), r[k]);
     if (a.y) {
+#pragma unroll
+      for (int k = 0; k < VPT; ++k) load<BT, VEC>(a.y, t * a.ldy + place(k), b[k]);
+      float token[1] = {0.f};
+      if (a.gate && !a.gate_col) load<BT, 1>(a.gate, t * a.gate_row, token);
       if (a.post_norm) norm(b, a.w_post, a.b_post);
+      if (a.gate) {
+        auto act = [&](float g) {
+          return a.gate_act == MOE_GATE_SIGMOID ? 1.f / (1.f + expf(-g)) : g;
+        };
+        token[0] = act(token[0]);
 #pragma unroll
-      for (int k = 0; k < VPT; ++k) {
-        const int i = i0 + k * step;
-        if (i < H) {
+        for (int k = 0; k < VPT; ++k) {
           float g[VEC];
+          if (a.gate_col) {
+            load<BT, VEC>(a.gate, t * a.gate_row + place(k), g);
 #pragma unroll
-          for (int j = 0; j < VEC; ++j) g[j] = 1.f;
-          if (a.gate) {
-            if (a.gate_col) {
-              load<BT, VEC>(a.gate, t * a.gate_row + i, g);
-            } else {
-              float one[1];
-              load<BT, 1>(a.gate, t * a.gate_row, one);
+            for (int j = 0; j < VEC; ++j) b[k][j] *= act(g[j]);
+          } else {
 #pragma unroll
-              for (int j = 0; j < VEC; ++j) g[j] = one[0];
-            }
-            if (a.gate_act == MOE_GATE_SIGMOID)
-#pragma unroll
-              for (int j = 0; j < VEC; ++j) g[j] = 1.f / (1.f + expf(-g[j]));
+            for (int j = 0; j < VEC; ++j) b[k][j] *= token[0];
           }
-#pragma unroll
-          for (int j = 0; j < VEC; ++j)
-            r[k][j] = a.res_scale * r[k][j] + a.branch_scale * (g[j] * b[k][j]);
         }
       }
+#pragma unroll
+      for (int k = 0; k < VPT; ++k)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j)
+          r[k][j] = a.res_scale * r[k][j] + a.branch_scale * b[k][j];
     } else {
 #pragma unroll
       for (int k = 0; k < VPT; ++k)
@@ -536,8 +539,12 @@ cudaError_t launch(const NormArgs& a, cudaStream_t s) {
   return launch_pdl(k_block_norm<RT, BT, VEC, VPT, MAXT>, a.T, threads, 0, s, a);
 }
 
-// Few rows: one access a thread, so that a row's loads leave together (the
-// call's latency).  More than the GPU holds at once: the kernel that stays.
+// Few rows: a CTA each, one access a thread where 1024 threads are enough, so that a
+// row's loads leave together (64 x 1001 f16 2.3 us, 3.5 with four accesses).  More than
+// two CTAs for every SM: the kernel that stays (4096 x 6144 fp32 / bf16 with norms on
+// both sides 54 us, 98 with a CTA a row); for rows that begin anywhere too, if all
+// tensors' begin alike and they are not short (2000 x 2049 bf16 16.8 us, 24.3 value by
+// value; 3000 x 4097 f16 44.8 and 93.5; but 4000 x 333 13.4 and 12.3).
 template <int RT, int BT>
 cudaError_t dispatch(const NormArgs& a, int vec, bool alike, cudaStream_t s) {
   const int H = a.H;
@@ -551,7 +558,7 @@ cudaError_t dispatch(const NormArgs& a, int vec, bool alike, cudaStream_t s) {
     if (H <= 8 * 2 * 1024) return launch<RT, BT, 8, 2, 1024>(a, s);
     return launch<RT, BT, 8, 4, 1024>(a, s);
   }
-  if (a.T > 2 * kSMs && alike) {
+  if (a.T > 2 * kSMs && H > 512 && alike) {
     cudaError_t e;
     if (launch_rows<RT, BT, 768, true>(a, s, e) || launch_rows<RT, BT, 1024, true>(a, s, e)) return e;
   }

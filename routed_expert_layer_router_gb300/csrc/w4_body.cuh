@@ -3,16 +3,22 @@
 //
 // y[t][n] = sum_G s[n][G] * sum_{k in G} (value(code) - zero) x[t][k] + bias[n]
 //
-// Bound by reading the codes once: half a byte a weight, so the instructions per
-// weight decide.  A warp takes 16 rows of W and every n-th chunk of 256 input
-// values; it streams its codes through its own ring of cp.async stages.  ldmatrix
-// on the raw codes hands a thread 8 consecutive codes of a row, four threads 32:
-// that is one scale group of 32 or a part of a larger one, so every group size
-// sums inside the matrix instructions in fp32 and the scale multiplies once a
-// group.
-// The warps that share a chunk (WR of them, for different rows) share its x in
-// shared memory.  The K split of a CTA (WK) and of a cluster is added up in a
-// fixed order at the end, the cluster's through distributed shared memory.
+// Half a byte a weight is read once for every 16 tokens.  What bounds it is less the
+// memory (1 x 6144 x 6144, groups of 128 with zero points: 7.7 us, 19.6 MB, 2.5 TB/s;
+// 13 x 8192 x 6144, groups of 64: 12.8 us, 27 MB, 2.1 TB/s) than the start of the call
+// and the instructions a code costs: a warp issues about 450 for a chunk of 16 rows x
+// 256 values, 16 of them matrix products with up to 8 tokens and 32 with 16.
+//
+// A warp takes 16 rows of W and every n-th chunk of 256 input values; it streams its
+// codes through its own ring of cp.async stages.  ldmatrix on the raw codes hands a
+// thread 8 consecutive codes of a row, four threads 32: that is one scale group of 32
+// or a part of a larger one, so every group size sums inside the matrix instructions
+// in fp32 and the scale multiplies once a group.  The warps that share a chunk (for
+// different rows) share its x in shared memory.  The K split of a CTA and of a cluster
+// is added up in a fixed order at the end, the cluster's through distributed shared
+// memory.  The products are 16 rows by 8 or 16 tokens of 16 values; tcgen05's tiles
+// of 64 rows and more would want the weights expanded into shared memory first, four
+// times their bytes.
 #pragma once
 
 #include <atomic>
@@ -31,7 +37,7 @@ struct W4Args {
   const uint8_t* zeros;
   const uint16_t* bias;
   uint16_t* y;
-  uint8_t* prepared;                   // [chunk][pass][17][kXPitch], or nullptr: prepared here
+  uint8_t* prepared;                   // [chunk][pass][17][kXPitch]: the workspace
   int64_t ldx, ldy;
 };
 
@@ -65,7 +71,7 @@ __device__ __forceinline__ int sum_place(int t) { return (t & 6) * 2 + (t >> 3) 
 //     its sums over each group are kept, with which the zero points come off:
 //     sum (n - zero) x = sum n x - zero sum x.
 // Subtracting zero points from every code instead, with packed 16-bit arithmetic,
-// took 9.3 us against REPLACE at 1 x 6144 x 6144.
+// took 9.3 us against 8.0 at 1 x 6144 x 6144.
 template <int DT, int FMT>
 constexpr bool kPrepares = DT == MOE_DT_BF16 || FMT == MOE_W4_U4;
 
@@ -157,7 +163,8 @@ __device__ __forceinline__ float cluster_load(uint32_t addr, uint32_t rank) {
   return v;
 }
 
-// Stages of a ring, and how many CTAs the GPU is given at once
+// Stages of a ring, and the CTAs of an SM that registers are kept for (with one CTA an
+// SM 1 x 6144 x 6144 takes 18.0 us against 7.7, 13 x 8192 x 6144 15.1 against 12.8)
 template <int NT>
 struct Shape {
   static constexpr int S = NT == 2 ? 4 : 3;
@@ -183,7 +190,7 @@ __global__ void __launch_bounds__(128) k_w4_prepare(W4Args a) {
 // 2 or 4, so that its ends are known at compile time and its scales come a chunk
 // ahead; 0: any.
 // FIX: 0, or warps along the rows that are known at compile time: 1, one token, or 8
-// with PRE (13 x 9216 x 6144: 12.9 us, 14.9 as one kernel with the others; 1 x 6144 x
+// with PRE (13 x 8192 x 6144: 12.8 us, 14.9 as one kernel with the others; 1 x 6144 x
 // 6144: 7.7 and 8.0).
 // PRE: x comes prepared from the workspace.  The kernel that prepares it is the one
 // before, and all before that one are done when this one starts, so the codes' and
