@@ -12,7 +12,7 @@ namespace {
 
 // ------------------------------------------------------------------ append
 // Bound by memory: q, k, v read once, q_out and the pages written once (4096 tokens
-// of 48 + 2 x 8 heads of 128 into 8-bit pages 26 us, 4.8 TB/s; one token 1.9 us).
+// of 48 + 2 x 8 heads of 128 into 8-bit pages 24 us, 5.3 TB/s; one token 1.8 us).
 // A CTA takes a token (and, for few tokens, a slice of its heads) at a time.  A
 // thread owns 16 values of a head - the 8 pairs that share 8 cosines and sines -
 // and walks the heads, so cos and sin are loaded once a token.
@@ -920,10 +920,16 @@ MOE_API moe_status kvcache_append(const kvcache_append_args* a, void* stream) {
   kvcache_append_args b = *a;
   if (!b.q) b.Hq = 0;
   if (!b.cos) b.rot = 0;
-  const int items = b.c.D / 16, lanes = kAppendThreads / items;
-  const int heads = b.Hq + 2 * b.c.Hkv;
+  // A token's place costs every warp of its CTA as much as one or two heads: CTAs of
+  // 128 threads once there are four tokens an SM (4096 tokens of 64 heads 26.3 -> 24.0
+  // us; but 300 of 56 heads 2.8 -> 3.1), and no more than the heads fill (4096 tokens of
+  // 6 heads of 64 10.4 -> 4.5 us).
+  const int items = b.c.D / 16, heads = b.Hq + 2 * b.c.Hkv;
+  const int most = (b.N < 4 * kSMs ? kAppendThreads : kAppendThreads / 2) / items;
+  const int lanes = heads < most ? heads : most;
+  const int held = 2048 / ((items * lanes + 31) / 32 * 32) * kSMs;  // CTAs, about
   const dim3 block(items, lanes);
-  const dim3 grid(b.N < 8 * kSMs ? b.N : 8 * kSMs, b.N < kSMs ? (heads + lanes - 1) / lanes : 1);
+  const dim3 grid(b.N < held ? b.N : held, b.N < kSMs ? (heads + lanes - 1) / lanes : 1);
   uint32_t mul, shift;
   page_divisor(b.c.page_size, &mul, &shift);
   cudaStream_t s = (cudaStream_t)stream;
