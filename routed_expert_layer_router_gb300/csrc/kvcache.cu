@@ -379,14 +379,24 @@ __global__ void __launch_bounds__(kWarps * 32, Ring<KV, DP, RH>::CTAS) k_attend(
       const uint32_t mask = __ballot_sync(~0u, ok) & ALL;
       if (lane == 0) valid[w][stage] = mask;
       const uint32_t kd = base + stage * R::STAGE, vd = kd + TOK * RB;
+      // the lanes of a row copy 128 bytes of it at a time, so that its place is handed
+      // over once
+      constexpr int LANES = CPR < 8 ? CPR : 8;
+      const int lr = lane / LANES, lc = lane % LANES;
 #pragma unroll
-      for (int i = 0; i < TOK * CPR / 32; ++i) {
-        const int idx = i * 32 + lane, row = idx / CPR, ch = idx % CPR;
-        const int64_t o = __shfl_sync(~0u, off, row) + ch * 16;
-        const bool v = ((mask >> row) & 1) && ch < nch;
-        const uint32_t d = R::at(row, ch);
-        cp_async16(kd + d, (const uint8_t*)a.c.k_pages + (v ? o : 0), v ? 16 : 0);
-        cp_async16(vd + d, (const uint8_t*)a.c.v_pages + (v ? o : 0), v ? 16 : 0);
+      for (int t = 0; t < TOK; t += 32 / LANES) {
+        const int row = t + lr;
+        const int64_t o = __shfl_sync(~0u, off, row) + lc * 16;
+        const bool v = (mask >> row) & 1;
+        const uint8_t* ks = (const uint8_t*)a.c.k_pages + o;
+        const uint8_t* vs = (const uint8_t*)a.c.v_pages + o;
+#pragma unroll
+        for (int j = 0; j < CPR / LANES; ++j) {
+          const uint32_t d = R::at(row, lc) ^ (j * LANES * 16);  // at(row, lc + j LANES)
+          const uint32_t bytes = v && lc + j * LANES < nch ? 16 : 0;
+          cp_async16(kd + d, ks + j * LANES * 16, bytes);
+          cp_async16(vd + d, vs + j * LANES * 16, bytes);
+        }
       }
       ++ui;
       if (ui < u1) ci.next(a, nh);
