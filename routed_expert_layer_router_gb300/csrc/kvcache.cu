@@ -516,131 +516,150 @@ __global__ void __launch_bounds__(kWarps * 32, Ring<KV, DP, RH>::CTAS) k_attend(
       l[r] += __shfl_xor_sync(~0u, l[r], 1);
       l[r] += __shfl_xor_sync(~0u, l[r], 2);
     }
+    auto output = [&]() {
+      const float vs = KV == MOE_DT_E4M3 && a.c.v_scale ? a.c.v_scale[kvh] : 1.f;
 #pragma unroll 1
-    for (bool whole = t0 == 0 && t1 == it.nt;; whole = true) {
+      for (int u = threadIdx.x; u < KS * ROWS; u += blockDim.x) {
+        const int row = u % ROWS, p = u / ROWS;  // 16 values of one head
+        const int head = hb * ROWS + row;
+        if (head >= a.G || p * 16 >= a.c.D) continue;
+        const float2 st = stat(row);
+        const float k = st.y == 0.f ? 0.f : vs / st.y;
+        float o[16];
 #pragma unroll
-      for (int r = 0; r < RH; ++r)
-        if (c4 == 0) ml[w][r * 8 + g] = make_float2(m[r], l[r]);
-      __syncthreads();
-      float f[RH];
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int r = 0; r < RH; ++r) f[r] = exp2_approx(m[r] - zero_if_empty(stat(r * 8 + g).x));
-#pragma unroll 1
-      for (int k = 0; k < rounds; ++k) {
-        if (turn == k) {
+          for (int j = 0; j < 2; ++j) {
+            const float4 x = sum4((((2 * p + i) * RH + (row >> 3)) * 2 + j) * 8 + (row & 7));
+            const float v[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-          for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int r = 0; r < RH; ++r)
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                float* p = mine + ((i * RH + r) * 2 + j) * 32 + lane;
-                const float v = RH == 1 ? (acc[i][j] + acc[i][2 + j]) * f[0] : acc[i][2 * r + j] * f[r];
-                *p = k ? *p + v : v;
-              }
-        }
-        __syncthreads();
-      }
-      if (whole) {
-        const float vs = KV == MOE_DT_E4M3 && a.c.v_scale ? a.c.v_scale[kvh] : 1.f;
-#pragma unroll 1
-        for (int u = threadIdx.x; u < KS * ROWS; u += blockDim.x) {
-          const int row = u % ROWS, p = u / ROWS;  // 16 values of one head
-          const int head = hb * ROWS + row;
-          if (head >= a.G || p * 16 >= a.c.D) continue;
-          const float2 st = stat(row);
-          const float k = st.y == 0.f ? 0.f : vs / st.y;
-          float o[16];
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const float4 x = sum4((((2 * p + i) * RH + (row >> 3)) * 2 + j) * 8 + (row & 7));
-              const float v[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                // see the V fragments: with 8-bit values tile i holds the even or odd ones
-                const int d = KV == MOE_DT_E4M3 ? 4 * c + 2 * j + i : 8 * i + 2 * c + j;
-                o[d] = v[c] * k;
-              }
+            for (int c = 0; c < 4; ++c) {
+              // see the V fragments: with 8-bit values tile i holds the even or odd ones
+              const int d = KV == MOE_DT_E4M3 ? 4 * c + 2 * j + i : 8 * i + 2 * c + j;
+              o[d] = v[c] * k;
             }
-          uint16_t* dst = (uint16_t*)a.out + it.b * a.out_row +
-                          (int64_t)(kvh * a.G + head) * a.out_head + p * 16;
-          uint32_t pk[8];
+          }
+        uint16_t* dst = (uint16_t*)a.out + it.b * a.out_row +
+                        (int64_t)(kvh * a.G + head) * a.out_head + p * 16;
+        uint32_t pk[8];
 #pragma unroll
-          for (int d = 0; d < 8; ++d)
-            pk[d] = a.q_bf16 ? pack_bf16(o[2 * d], o[2 * d + 1]) : pack_f16(o[2 * d], o[2 * d + 1]);
-          ((uint4*)dst)[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-          ((uint4*)dst)[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
-          if (p == 0 && a.lse)
-            a.lse[(int64_t)it.b * a.Hq + kvh * a.G + head] = (st.x + (log2f(st.y) - LIFT)) * (1.f / kLog2e);
-        }
-        return;
+        for (int d = 0; d < 8; ++d)
+          pk[d] = a.q_bf16 ? pack_bf16(o[2 * d], o[2 * d + 1]) : pack_f16(o[2 * d], o[2 * d + 1]);
+        ((uint4*)dst)[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+        ((uint4*)dst)[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+        if (p == 0 && a.lse)
+          a.lse[(int64_t)it.b * a.Hq + kvh * a.G + head] = (st.x + (log2f(st.y) - LIFT)) * (1.f / kLog2e);
       }
-      // part p of the item comes from run cs + p; the first is that run's last
-      // piece, any other its run's first
-      auto run_of = [&](int u) {
-        const int longer = more * (each + 1);
-        return u < longer ? u / (each + 1) : more + (u - longer) / each;
-      };
-      const int cs = run_of(first_u), np = run_of(first_u + it.nt - 1) - cs + 1;
-      auto part = [&](int p) {
-        return a.parts + (size_t)(p == 0 ? 2 * cs + 1 : 2 * (cs + p)) * PART;
-      };
-      float* to = part(cta - cs);
+    };
+#pragma unroll
+    for (int r = 0; r < RH; ++r)
+      if (c4 == 0) ml[w][r * 8 + g] = make_float2(m[r], l[r]);
+    __syncthreads();
+    float f[RH];
+#pragma unroll
+    for (int r = 0; r < RH; ++r) f[r] = exp2_approx(m[r] - zero_if_empty(stat(r * 8 + g).x));
 #pragma unroll 1
-      for (int i = threadIdx.x; i < SLICE / 4; i += blockDim.x) ((float4*)to)[i] = sum4(i);
-      if (threadIdx.x < ROWS) ((float2*)(to + SLICE))[threadIdx.x] = stat(threadIdx.x);
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        // releases the CTA's part, which the barrier has gathered, and takes the others'
-        unsigned done;
-        asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;"
-                     : "=r"(done)
-                     : "l"(a.counters + cs)
-                     : "memory");
-        is_last = done == (unsigned)np - 1;
-        if (is_last) a.counters[cs] = 0;
-      }
-      __syncthreads();
-      if (!is_last) return;
-      // The last part has come.  Each warp adds every fourth part to its registers
-      // under a running maximum, so that all loads leave at once; the warps then
-      // meet as before.
-#pragma unroll
-      for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-#pragma unroll
-      for (int r = 0; r < RH; ++r) m[r] = NEG_INF, l[r] = 0.f;
-#pragma unroll 1
-      for (int p = w; p < np; p += kWarps) {
-        const float* from = part(p);
-        float v[NT][RH][2];
-        float2 st[RH];
-#pragma unroll
-        for (int r = 0; r < RH; ++r) st[r] = __ldcg((const float2*)(from + SLICE) + r * 8 + g);
+    for (int k = 0; k < rounds; ++k) {
+      if (turn == k) {
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
           for (int r = 0; r < RH; ++r)
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-              v[i][r][j] = __ldcg(from + ((i * RH + r) * 2 + j) * 32 + lane);
+            for (int j = 0; j < 2; ++j) {
+              float* p = mine + ((i * RH + r) * 2 + j) * 32 + lane;
+              const float v = RH == 1 ? (acc[i][j] + acc[i][2 + j]) * f[0] : acc[i][2 * r + j] * f[r];
+              *p = k ? *p + v : v;
+            }
+      }
+      __syncthreads();
+    }
+    if (t0 == 0 && t1 == it.nt) {
+      output();
+      return;
+    }
+    // part p of the item comes from run cs + p; the first is that run's last
+    // piece, any other its run's first
+    auto run_of = [&](int u) {
+      const int longer = more * (each + 1);
+      return u < longer ? u / (each + 1) : more + (u - longer) / each;
+    };
+    const int cs = run_of(first_u), np = run_of(first_u + it.nt - 1) - cs + 1;
+    auto part = [&](int p) {
+      return a.parts + (size_t)(p == 0 ? 2 * cs + 1 : 2 * (cs + p)) * PART;
+    };
+    float* to = part(cta - cs);
+#pragma unroll 1
+    for (int i = threadIdx.x; i < SLICE / 4; i += blockDim.x) ((float4*)to)[i] = sum4(i);
+    if (threadIdx.x < ROWS) ((float2*)(to + SLICE))[threadIdx.x] = stat(threadIdx.x);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      // releases the CTA's part, which the barrier has gathered, and takes the others'
+      unsigned done;
+      asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;"
+                   : "=r"(done)
+                   : "l"(a.counters + cs)
+                   : "memory");
+      is_last = done == (unsigned)np - 1;
+      if (is_last) a.counters[cs] = 0;
+    }
+    __syncthreads();
+    if (!is_last) return;
+    // The last part has come.  Each warp adds every fourth part to its registers under a
+    // running maximum, as many parts' loads at once as its registers take; the warps then
+    // meet as before.  A lane's four values of a load belong to one row.  (2 x 5000
+    // tokens, 16 heads a kv head: 16.8 us with single values and a part at a time, 16.0.)
+    constexpr int F4 = NT * RH / 2, F = RH == 1 && F4 > 8 ? 8 : F4;
+    constexpr int BATCH = (NT == 32 ? 32 : 16) / F;
+    const int row = (RH == 2 ? lane >> 4 << 3 : 0) + (lane & 7);
+#pragma unroll 1
+    for (int first = 0; first < F4; first += F) {  // of a lane's loads, 8 at a time
+      float4 sum[F];
+      float2 at = make_float2(NEG_INF, 0.f);  // its row's maximum and sum
 #pragma unroll
-        for (int r = 0; r < RH; ++r) {
-          const float top = fmaxf(m[r], st[r].x), z = zero_if_empty(top);
-          const float old = exp2_approx(m[r] - z), e = exp2_approx(st[r].x - z);
-          m[r] = top;
-          l[r] = l[r] * old + st[r].y * e;
+      for (int i = 0; i < F; ++i) sum[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+      for (int p = w; p < np; p += kWarps * BATCH) {
+        float4 v[BATCH][F];
+        float2 st[BATCH];
 #pragma unroll
-          for (int i = 0; i < NT; ++i)
+        for (int q = 0; q < BATCH; ++q) {
+          const float* from = part(min(p + q * kWarps, np - 1));
+          st[q] = __ldcg((const float2*)(from + SLICE) + row);
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-              acc[i][2 * r + j] = acc[i][2 * r + j] * old + e * v[i][r][j];
+          for (int i = 0; i < F; ++i) v[q][i] = __ldcg((const float4*)from + (first + i) * 32 + lane);
+        }
+#pragma unroll
+        for (int q = 0; q < BATCH; ++q) {
+          if (p + q * kWarps >= np) break;
+          const float top = fmaxf(at.x, st[q].x), z = zero_if_empty(top);
+          const float old = exp2_approx(at.x - z), e = exp2_approx(st[q].x - z);
+          at = make_float2(top, at.y * old + st[q].y * e);
+#pragma unroll
+          for (int i = 0; i < F; ++i) {
+            sum[i].x = sum[i].x * old + e * v[q][i].x, sum[i].y = sum[i].y * old + e * v[q][i].y;
+            sum[i].z = sum[i].z * old + e * v[q][i].z, sum[i].w = sum[i].w * old + e * v[q][i].w;
+          }
         }
       }
+      if (first == 0 && (lane & 8) == 0 && (RH == 2 || lane < 8)) ml[w][row] = at;
+      __syncthreads();
+      const float scale = exp2_approx(at.x - zero_if_empty(stat(row).x));
+#pragma unroll 1
+      for (int k = 0; k < rounds; ++k) {
+        if (turn == k) {
+#pragma unroll
+          for (int i = 0; i < F; ++i) {
+            float4* p = (float4*)mine + (first + i) * 32 + lane;
+            const float4 o = k ? *p : make_float4(0.f, 0.f, 0.f, 0.f);
+            *p = make_float4(o.x + sum[i].x * scale, o.y + sum[i].y * scale,
+                             o.z + sum[i].z * scale, o.w + sum[i].w * scale);
+          }
+        }
+        __syncthreads();
+      }
     }
+    output();
   };
 
   {
