@@ -497,7 +497,8 @@ __global__ void __launch_bounds__(MAXT) k_block_norm_rows(NormArgs a, int stages
   cp_async_wait<0>();
 }
 
-// false where a row is too long for it
+// false where a row is too long for it: more than MAXT threads, or two stages of pairs
+// past shared memory (fp32 throughout, from 4672 values with a gate a value, 7168 without)
 template <int RT, int BT, int MAXT, bool ODD>
 bool launch_rows(const NormArgs& a, cudaStream_t s, cudaError_t& e) {
   static_assert(kSMs % 8 == 0, "rows of a CTA");
@@ -527,6 +528,7 @@ bool launch_rows(const NormArgs& a, cudaStream_t s, cudaError_t& e) {
   int stages = kMost / per_sm / pair;
   stages = stages > 4 ? 4 : stages < 2 ? 2 : stages;
   while (per_sm > 1 && per_sm * (stages * pair + 1536) > 227 * 1024) --per_sm;
+  if (stages * pair > kMost) return false;
   const int pairs = (a.T + 1) / 2;
   const int most = per_sm * kSMs, few = ODD ? (pairs + 7) / 8 * 8 : pairs;
   e = launch_pdl(kern, few < most ? few : most, threads, (size_t)stages * pair, s, a, stages);

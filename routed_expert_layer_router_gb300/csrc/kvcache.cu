@@ -146,8 +146,8 @@ __global__ void __launch_bounds__(kAppendThreads, 4)
 
 // ------------------------------------------------------------------ attend
 // Bound by reading the cache once (one sequence of 131075 tokens of 8 x 128 values in
-// bf16 90 us, 6.0 TB/s; 32 ragged ones in 8 bits 96 us, 5.6 TB/s), and for short
-// ones by the chain of dependent loads (777 tokens 7.5 us).  Scores are kept in units
+// bf16 88 us, 6.1 TB/s; 32 ragged ones in 8 bits 94 us, 5.7 TB/s), and for short
+// ones by the chain of dependent loads (777 tokens 7.2 us).  Scores are kept in units
 // of log2, times log2(e), so that each weight is one exp2; the running maximum and sum
 // of a row are joined by exp2 of the maxima's difference.  The tokens are cut into tiles
 // of 64 or 128; the tiles of all (sequence, kv head) items in a row are dealt to
@@ -278,8 +278,10 @@ __global__ void __launch_bounds__(kWarps * 32, Ring<KV, DP, RH>::CTAS) k_attend(
   // ---- this CTA's run [u0, u1) of the U tiles: U / ctas each, the first U % ctas
   // one more.  A CTA more costs an item's join another part, a tile more costs its
   // CTA the tile: runs of at least about sqrt(n / 8) tiles for items of n (777
-  // tokens 7.6 us, against 9.7 with sqrt(n / 2); 32000 tokens in 8 bits 21.5,
-  // against 29.7, and 26.2 with runs of one tile).
+  // tokens 7.5 us, against 9.6 with sqrt(n / 2); 32000 tokens in 8 bits 20.5,
+  // against 30.8, and 26.2 with runs of one tile).  Cutting every item by itself, so
+  // that no CTA holds the ends of two, cost more index work than it saved (8.0 us;
+  // 4 x 9000 tokens of 2 x 256 values 27.7 against 24.4).
   Span s0 = {0, 0};
   if (lane < a.B) s0 = span_of(a, lane);
   const int n0 = tiles_of<TILE>(s0);

@@ -14,7 +14,7 @@ using namespace moe;
 
 MOE_API size_t moe_w4_linear_workspace_bytes(int T, int K, int dtype, int format) {
   if (T <= 8 || K <= 0 || (dtype == MOE_DT_F16 && format == MOE_W4_E2M1)) return 0;
-  return (size_t)((K + kChunk - 1) / kChunk) * ((T + kTokens - 1) / kTokens) * kPass;
+  return (size_t)((K + kChunk - 1) / kChunk) * T * kXPitch;
 }
 
 MOE_API moe_status moe_w4_linear(const moe_w4_linear_args* a, void* stream) {
@@ -30,8 +30,9 @@ MOE_API moe_status moe_w4_linear(const moe_w4_linear_args* a, void* stream) {
     return MOE_ERR_UNSUPPORTED;
   if (a->T > 4 * 65535) return MOE_ERR_UNSUPPORTED;  // the grids' second dimension
   const size_t need = moe_w4_linear_workspace_bytes(a->T, a->K, a->dtype, a->format);
-  if (need && (!a->workspace || a->workspace_bytes < need)) return MOE_ERR_INVALID_ARG;
+  if (need && !a->workspace) return MOE_ERR_INVALID_ARG;
   if (need && ((uintptr_t)a->workspace & 15)) return MOE_ERR_UNSUPPORTED;
+  if (need && a->workspace_bytes < need) return MOE_ERR_INVALID_ARG;
   W4Args k;
   k.T = a->T, k.N = a->N, k.K = a->K, k.G = a->K / a->group, k.g32 = a->group / 32;
   k.zrow = a->zeros ? (k.G + 1) / 2 : 0;

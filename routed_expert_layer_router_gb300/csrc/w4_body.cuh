@@ -37,7 +37,7 @@ struct W4Args {
   const uint8_t* zeros;
   const uint16_t* bias;
   uint16_t* y;
-  uint8_t* prepared;                   // [chunk][pass][17][kXPitch]: the workspace
+  uint8_t* prepared;                   // the workspace: [chunk][T] values, [chunk][pass] sums
   int64_t ldx, ldy;
 };
 
@@ -47,15 +47,15 @@ constexpr int kChunk = 256;            // input values of a stage: 128 bytes of 
 constexpr int kMostCtas = 8;           // of a cluster
 constexpr int kMostSmem = 224 * 1024, kSmSmem = 228 * 1024;  // of a CTA, of an SM
 constexpr int kTokens = 16;            // tokens of one pass over the weights
-// A chunk of x, in shared memory and in the workspace: a row of group sums and of
-// what undoes each token's power of two, then a row for each token's 256 values
-// (prepared: f16).  The 64 bytes past the values put two tokens' reads into different
-// bank halves.  A row of sums holds 8 groups (or blocks of 32) of 16 tokens, then the
+// A chunk of x in shared memory: a row of group sums and of what undoes each token's
+// power of two, then a row for each token's 256 values (prepared: f16).  The 64 bytes
+// past the values put two tokens' reads into different bank halves; in the workspace
+// values and sums lie apart, without them.  A row of sums holds 8 groups (or blocks of 32) of 16 tokens, then the
 // 16 tokens' powers, the tokens in the order in which a thread of the matrix
 // instructions wants its two or four together.
 constexpr int kXPitch = kChunk * 2 + 64;
 constexpr int kUndo = 8 * kTokens;
-constexpr int kPass = (kTokens + 1) * kXPitch;  // of the workspace
+constexpr int kValues = kChunk * 2, kSumRow = kXPitch;  // bytes in the workspace
 static_assert((kUndo + kTokens) * 4 <= kXPitch, "a row of sums");
 __device__ __forceinline__ int sum_place(int t) { return (t & 6) * 2 + (t >> 3) * 2 + (t & 1); }
 
@@ -118,14 +118,14 @@ __device__ __forceinline__ float prepare_x(uint4& v, float& sum) {
   return __uint_as_float((uint32_t)(127 - up) << 23);
 }
 
-// the same for token t of a chunk at `to`, with its sums; g32: the group's length in
-// blocks of 32 where it is 1, 2 or 4, else sums are of blocks
+// the same for token t of a pass, its values to `to`, its sums into their row; g32: the
+// group's length in blocks of 32 where it is 1, 2 or 4, else sums are of blocks
 template <int DT, int FMT>
-__device__ __forceinline__ void prepare_chunk(uint4 v, int g32, uint8_t* to, int t, int lane) {
+__device__ __forceinline__ void prepare_chunk(uint4 v, int g32, uint8_t* to, float* row, int t, int lane) {
   float sum;
   const float undo = prepare_x<DT, FMT>(v, sum);
-  *(uint4*)(to + (t + 1) * kXPitch + lane * 16) = v;
-  float* row = (float*)to + sum_place(t);
+  *(uint4*)(to + lane * 16) = v;
+  row += sum_place(t);
   if constexpr (FMT == MOE_W4_U4) {
     // lanes 4 i .. 4 i + 3 hold block i
     const int per = g32 == 2 || g32 == 4 ? 4 * g32 : 4;
@@ -182,8 +182,10 @@ __global__ void __launch_bounds__(128) k_w4_prepare(W4Args a) {
   uint4 v = make_uint4(0, 0, 0, 0);
   if (k < a.K) v = *(const uint4*)(a.x + t * a.ldx + k);
   const int passes = (a.T + kTokens - 1) / kTokens;
-  uint8_t* to = a.prepared + ((int64_t)kc * passes + t / kTokens) * kPass;
-  prepare_chunk<DT, FMT>(v, a.g32, to, t % kTokens, lane);
+  uint8_t* sums = a.prepared + (int64_t)gridDim.x * a.T * kValues;
+  prepare_chunk<DT, FMT>(v, a.g32, a.prepared + ((int64_t)kc * a.T + t) * kValues,
+                         (float*)(sums + ((int64_t)kc * passes + t / kTokens) * kSumRow),
+                         t % kTokens, lane);
 }
 
 // NT: token tiles of 8.  G32: the group's length in blocks of 32 values where it is 1,
@@ -279,10 +281,15 @@ __global__ void __launch_bounds__(256, Shape<NT>::PER_SM) k_w4(W4Args a) {
   auto issue_x = [&](int kc, int stage) {
     if (kc >= chunks) return;
     if constexpr (PRE) {
-      const uint8_t* from = a.prepared + ((int64_t)kc * gridDim.y + blockIdx.y) * kPass;
+      const uint8_t* from = a.prepared + ((int64_t)kc * a.T + t0) * kValues + lane * 16;
+      const uint8_t* sums = a.prepared + (int64_t)chunks * a.T * kValues +
+                            ((int64_t)kc * gridDim.y + blockIdx.y) * kSumRow;
       const uint32_t to = ptx::smem_u32(xbase) + stage * xstage;
+      const int i = (wr * 32 + lane) * 16;
+      if (i < kSumRow) cp_async16(to + i, sums + i, 16);
 #pragma unroll 1
-      for (int i = (wr * 32 + lane) * 16; i < xstage; i += WR * 512) cp_async16(to + i, from + i, 16);
+      for (int t = wr; t < nt; t += WR)
+        cp_async16(to + (t + 1) * kXPitch + lane * 16, from + t * kValues, 16);
     } else {
       const bool xin = kc * kChunk + lane * 8 < a.K;
       const uint16_t* xs = xin ? xsrc + (int64_t)kc * kChunk : a.x;
@@ -352,8 +359,8 @@ __global__ void __launch_bounds__(256, Shape<NT>::PER_SM) k_w4(W4Args a) {
       if constexpr (!PRE) {
 #pragma unroll 1
         for (int t = wr; t < nt; t += WR) {
-          const uint8_t* p = xc + (t + 1) * kXPitch;
-          prepare_chunk<DT, FMT>(*(const uint4*)(p + lane * 16), G32, xc, t, lane);
+          uint8_t* p = xc + (t + 1) * kXPitch;
+          prepare_chunk<DT, FMT>(*(const uint4*)(p + lane * 16), G32, p, (float*)xc, t, lane);
         }
         group_sync();
       }
@@ -565,7 +572,8 @@ moe_status shape_w4(W4Args a, cudaStream_t s) {
   const int chunks = (a.K + kChunk - 1) / kChunk;
   const int passes = (a.T + kTokens - 1) / kTokens;
   const int nt = a.T < NT * 8 ? a.T : NT * 8;
-  constexpr bool prepares = kPrepares<DT, FMT> && NT == 2;
+  // the workspace, kXPitch a token and chunk, holds the sums' rows but for 17 tokens
+  const bool prepares = kPrepares<DT, FMT> && NT == 2 && passes * kSumRow <= a.T * (kXPitch - kValues);
   bool before = false;
   int tiles = 0, cluster = 1, smem = 0, least = 0;
   for (int wr_log = 3; wr_log >= 0; --wr_log) {
@@ -592,7 +600,7 @@ moe_status shape_w4(W4Args a, cudaStream_t s) {
     }
   }
   const dim3 grid(tiles * cluster, passes);
-  if constexpr (prepares) {
+  if constexpr (kPrepares<DT, FMT> && NT == 2) {
     if (before) {
       const cudaError_t e = launch_pdl(k_w4_prepare<DT, FMT>, dim3(chunks, (a.T + 3) / 4), 128, 0, s, a);
       if (e != cudaSuccess) return launch_status(e);

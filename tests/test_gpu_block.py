@@ -149,6 +149,53 @@ def test_norm_strides_and_in_place(block):
     check_norm(block, t, t, post=True)
 
 
+@pytest.mark.parametrize("stream,branch", [(BF, BF), (F16, F16), (F32, F32), (F32, BF), (F32, F16)])
+@pytest.mark.parametrize("T,H", [(320, 8192), (333, 5000), (401, 6001), (310, 8185), (305, 2049),
+                                 (1000, 515), (306, 802), (500, 333)])
+def test_norm_many_rows(block, stream, branch, T, H):
+    """More rows than the GPU has CTAs for, aligned or beginning anywhere."""
+    g = gen(T + H)
+    x, y = rn(g, T, H, dtype=stream, s=3.0), rn(g, T, H, dtype=branch)
+    w = rn(g, H, s=0.2) + 1
+    check_norm(block, x, y, "rms", w_pre=w, w_post=w, gate=rn(g, T, H, dtype=branch), sig=True, rs=0.5)
+    check_norm(block, x, y, "layer", w_pre=w.to(branch), b_pre=rn(g, H, dtype=branch),
+               b_post=rn(g, H, dtype=branch), gate=rn(g, H, dtype=branch), bs=-1.5, off=1.0)
+    check_norm(block, x, None, "layer", need_r=False, h_dtype=branch)
+
+
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("stream,branch", [(BF, BF), (F32, F16), (F32, F32)])
+def test_norm_many_odd_rows_stay_apart(block, kind, stream, branch):
+    """Rows that share aligned accesses with their neighbours: what lies beside a row
+    neither changes it nor is written, in place or not."""
+    g, T, H = gen(11), 331, 1001
+    big = [rn(g, T, H + 8, dtype=d) for d in (stream, branch, stream, branch)]
+    x, y, r, h = (t[:, :H] for t in big)
+    edge = [t[:, H:].clone() for t in big]
+    gate = rn(g, T, 1, dtype=branch)
+    kw = dict(kind=kind, post_norm=True, gate=gate, w_pre=rn(g, H))
+    check_norm(block, x, y, kind, post=True, gate=gate, w_pre=kw["w_pre"], r=r, h=h)
+    for t, e in zip(big, edge):
+        assert torch.equal(t[:, H:], e)
+    xd, yd = x.contiguous(), y.contiguous()
+    want = [t.clone() for t in (r, h)]
+    r1, h1 = block.block_norm(xd, yd, **kw)
+    assert torch.equal(r1, want[0]) and torch.equal(h1, want[1])
+    bad = torch.zeros(T, dtype=torch.bool, device="cuda")
+    for i, v in ((0, INF), (7, math.nan), (100, -INF), (330, math.nan)):
+        (xd if i % 2 else yd)[i, (i * 37) % H] = v
+        bad[i] = True
+    gate[200] = INF
+    bad[200] = True
+    r2, h2 = block.block_norm(xd, yd, **kw)
+    assert torch.equal(r2[~bad], want[0][~bad]) and torch.equal(h2[~bad], want[1][~bad])
+    assert not r2[bad].isfinite().all(-1).any()
+    gate[200] = 1.0
+    block.block_norm(x, y, r=x, h=y, **kw)
+    ok = torch.arange(T, device="cuda") != 200
+    assert torch.equal(x[ok], want[0][ok]) and torch.equal(y[ok], want[1][ok])
+
+
 def test_norm_extreme_rows(block):
     g, H = gen(3), 768
     x = rn(g, 6, H)
