@@ -741,14 +741,16 @@ __global__ void __launch_bounds__(kWarps * 32, Ring<KV, DP, RH>::CTAS) k_attend(
 #pragma unroll
     for (int r = 0; r < RH; ++r) {
       if (a.softcap > 0.f) {
-        // cap * tanh(v / cap) = cap * (1 - 2 / (e^(2 v / cap) + 1)): its error is
-        // a few 2^-24 of the cap, as absolute as the softmax takes it
+        // cap * tanh(v / cap) = +-cap (1 - e) / (1 + e), e = e^(-2 |v| / cap): its error is
+        // that of e, 2^-24 or so of the cap, as absolute as the softmax takes it
         const float in = sc[r] * (2.f * kLog2e / a.softcap), cap = a.softcap * kLog2e;
 #pragma unroll
         for (int i = 0; i < TT; ++i)
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
-            s[i][2 * r + j] = cap - 2.f * cap * rcp_approx(exp2_approx(s[i][2 * r + j] * in) + 1.f);
+          for (int j = 0; j < 2; ++j) {
+            const float x = s[i][2 * r + j] * in, e = exp2_approx(-fabsf(x));
+            s[i][2 * r + j] = copysignf(cap * (1.f - e) * rcp_approx(1.f + e), x);
+          }
       } else {
         const float k = sc[r] * kLog2e;
 #pragma unroll
