@@ -675,6 +675,21 @@ def test_w4_large(block, fmt, zeros, T, N, K, group):
 
 
 @pytest.mark.parametrize("dtype", [BF, F16])
+@pytest.mark.parametrize("fmt,zeros", [("u4", True), ("e2m1", False)])
+@pytest.mark.parametrize("T,N,K,group", [(40, 2000, 6144, 64), (17, 4000, 4096, 32), (33, 300, 8192, 128),
+                                         (4, 512, 8192, 64), (2, 6144, 1024, 32), (13, 512, 8160, 96),
+                                         (100, 4096, 2048, 128), (16, 8192, 4096, 256)])
+def test_w4_splits(block, dtype, fmt, zeros, T, N, K, group):
+    """Rows and K dealt to warps, CTAs and clusters in every way; x prepared before."""
+    g = gen(T + N)
+    codes, scales, z, bias = make_w4(g, N, K, group, dtype, fmt, zeros, True)
+    x = rn(g, T, K, dtype=dtype)
+    y = check_w4(block, x, codes, scales, z, bias, group, fmt)
+    lin = block.W4Linear(codes, scales, group, zeros=z, bias=bias, fmt=fmt)
+    assert torch.equal(y, lin.forward(x))
+
+
+@pytest.mark.parametrize("dtype", [BF, F16])
 @pytest.mark.parametrize("fmt", ["u4", "e2m1"])
 def test_w4_each_code_at_each_place(block, dtype, fmt):
     """x a unit vector: y is one column of W, exactly (scale 1)."""
