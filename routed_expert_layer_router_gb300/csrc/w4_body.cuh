@@ -5,7 +5,7 @@
 //
 // Half a byte a weight is read once for every 16 tokens.  What bounds it is less the
 // memory (1 x 6144 x 6144, groups of 128 with zero points: 7.7 us, 19.6 MB, 2.5 TB/s;
-// 13 x 8192 x 6144, groups of 64: 12.8 us, 27 MB, 2.1 TB/s) than the start of the call
+// 13 x 8192 x 6144, groups of 64: 13.2 us, 27 MB, 2.0 TB/s) than the start of the call
 // and the instructions a code costs: a warp issues about 450 for a chunk of 16 rows x
 // 256 values, 16 of them matrix products with up to 8 tokens and 32 with 16.
 //
@@ -287,9 +287,10 @@ __global__ void __launch_bounds__(256, Shape<NT>::PER_SM) k_w4(W4Args a) {
       const uint32_t to = ptx::smem_u32(xbase) + stage * xstage;
       const int i = (wr * 32 + lane) * 16;
       if (i < kSumRow) cp_async16(to + i, sums + i, 16);
-#pragma unroll 1
-      for (int t = wr; t < nt; t += WR)
-        cp_async16(to + (t + 1) * kXPitch + lane * 16, from + t * kValues, 16);
+#pragma unroll
+      for (int k = 0; k < kTokens; k += 8)  // of WR == 8 warps
+        if (wr + k < nt)
+          cp_async16(to + (wr + k + 1) * kXPitch + lane * 16, from + (wr + k) * kValues, 16);
     } else {
       const bool xin = kc * kChunk + lane * 8 < a.K;
       const uint16_t* xs = xin ? xsrc + (int64_t)kc * kChunk : a.x;
