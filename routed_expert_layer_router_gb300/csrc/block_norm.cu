@@ -498,7 +498,8 @@ __global__ void __launch_bounds__(MAXT) k_block_norm_rows(NormArgs a, int stages
 }
 
 // false where a row is too long for it: more than MAXT threads, or two stages of pairs
-// past shared memory (fp32 throughout, from 4672 values with a gate a value, 7168 without)
+// past shared memory (fp32 throughout, more than 4608 values with a gate a value, 7168
+// without)
 template <int RT, int BT, int MAXT, bool ODD>
 bool launch_rows(const NormArgs& a, cudaStream_t s, cudaError_t& e) {
   static_assert(kSMs % 8 == 0, "rows of a CTA");
@@ -562,7 +563,8 @@ cudaError_t dispatch(const NormArgs& a, int vec, bool alike, cudaStream_t s) {
   }
   if (a.T > 2 * kSMs && H > 512 && alike) {
     cudaError_t e;
-    if (launch_rows<RT, BT, 768, true>(a, s, e) || launch_rows<RT, BT, 1024, true>(a, s, e)) return e;
+    if (launch_rows<RT, BT, 768, true>(a, s, e) || launch_rows<RT, BT, 1024, true>(a, s, e))
+      return e;
   }
   if (vec == 2) {
     if (H <= 2 * 1024 && a.T <= 2 * kSMs) return launch<RT, BT, 2, 1, 1024>(a, s);

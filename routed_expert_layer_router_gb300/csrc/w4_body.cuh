@@ -50,9 +50,9 @@ constexpr int kTokens = 16;            // tokens of one pass over the weights
 // A chunk of x in shared memory: a row of group sums and of what undoes each token's
 // power of two, then a row for each token's 256 values (prepared: f16).  The 64 bytes
 // past the values put two tokens' reads into different bank halves; in the workspace
-// values and sums lie apart, without them.  A row of sums holds 8 groups (or blocks of 32) of 16 tokens, then the
-// 16 tokens' powers, the tokens in the order in which a thread of the matrix
-// instructions wants its two or four together.
+// values and sums lie apart, without them.  A row of sums holds 8 groups (or blocks of
+// 32) of 16 tokens, then the 16 tokens' powers, the tokens in the order in which a
+// thread of the matrix instructions wants its two or four together.
 constexpr int kXPitch = kChunk * 2 + 64;
 constexpr int kUndo = 8 * kTokens;
 constexpr int kValues = kChunk * 2, kSumRow = kXPitch;  // bytes in the workspace
@@ -566,6 +566,7 @@ moe_status shape_w4(W4Args a, cudaStream_t s) {
   // 12.6, 22.3; 13 x 512 x 8192: 8.0, 6.1, 9.5 with 2; 1 x 6144 x 6144: 8.8, 9.2, 9.1,
   // 8.0.)  Two CTAs an SM of clusters of 6 do not pack (16 tokens, 6144 x 6144: 18 us,
   // 13.5 in fours).
+  //
   // x of more than 8 tokens prepared by a kernel before costs a launch, and saves each of
   // the 8 warps that share it two tokens a chunk: from two chunks a warp on (16 tokens,
   // groups of 128, 8192 x 4096: 11.3 -> 9.7 us; 13, groups of 64, 4096 x 4096: 7.2 ->
