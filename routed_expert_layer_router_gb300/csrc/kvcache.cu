@@ -501,16 +501,17 @@ __global__ void __launch_bounds__(kWarps * 32, Ring<KV, DP, RH>::CTAS) k_attend(
     const int turn = idle ? 0 : RH == 1 ? 1 - (w >> 1) : kWarps - 1 - w;
     float* mine = idle ? (float*)(ring + w * R::WARP) : mb + (RH == 1 ? (w & 1) * SLICE : 0);
     const float* slices = idle ? (const float*)ring : mb;
-    const int nslice = idle ? kWarps : RH == 1 ? 2 : 1, pitch = idle ? R::WARP / 4 : SLICE;
-    auto sum4 = [&](int i) {  // floats 4 i .. 4 i + 3 of the sums
-      float4 x = *(const float4*)(slices + 4 * i);
-#pragma unroll
-      for (int k = 1; k < kWarps; ++k) {
-        if (k >= nslice) break;
-        const float4 y = *(const float4*)(slices + k * pitch + 4 * i);
-        x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
-      }
-      return x;
+    const int pitch = idle ? R::WARP / 4 : SLICE;
+    // floats 4 i .. 4 i + 3 of the sums, the warps in one order, (2 + 0) + (3 + 1) or
+    // ((3 + 2) + 1) + 0, whether the ring is idle or not: that depends, for a split row,
+    // on which CTA finishes last
+    auto sum4 = [&](int i) {
+      auto of = [&](int k) { return *(const float4*)(slices + k * pitch + 4 * i); };
+      auto plus = [](const float4& x, const float4& y) {
+        return make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+      };
+      if constexpr (RH == 1) return idle ? plus(plus(of(2), of(0)), plus(of(3), of(1))) : plus(of(0), of(1));
+      else return idle ? plus(plus(plus(of(3), of(2)), of(1)), of(0)) : of(0);
     };
     const int kvh = it.h / a.nhb, hb = it.h - kvh * a.nhb;
 #pragma unroll
@@ -653,9 +654,15 @@ __global__ void __launch_bounds__(kWarps * 32, Ring<KV, DP, RH>::CTAS) k_attend(
 #pragma unroll
           for (int i = 0; i < F; ++i) {
             float4* p = (float4*)mine + (first + i) * 32 + lane;
-            const float4 o = k ? *p : make_float4(0.f, 0.f, 0.f, 0.f);
-            *p = make_float4(o.x + sum[i].x * scale, o.y + sum[i].y * scale,
-                             o.z + sum[i].z * scale, o.w + sum[i].w * scale);
+            // (rounded products, as in slices of their own)
+            float4 x = make_float4(__fmul_rn(sum[i].x, scale), __fmul_rn(sum[i].y, scale),
+                                   __fmul_rn(sum[i].z, scale), __fmul_rn(sum[i].w, scale));
+            if (k) {
+              const float4 o = *p;
+              x = make_float4(__fadd_rn(o.x, x.x), __fadd_rn(o.y, x.y), __fadd_rn(o.z, x.z),
+                              __fadd_rn(o.w, x.w));
+            }
+            *p = x;
           }
         }
         __syncthreads();

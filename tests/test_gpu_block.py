@@ -349,6 +349,23 @@ def test_attend_split_and_joined(block, B, Hkv, length):
     check_attend(block, rn(g, B, Hkv * 4, D, dtype=BF), k, v, table_for(g, lens, page, n), lens)
 
 
+@pytest.mark.parametrize("dtype,kv", [(F16, F16), (BF, F8)])
+@pytest.mark.parametrize("G,D", [(16, 224), (4, 128), (16, 128), (12, 64), (1, 64)])
+def test_attend_same_bits_every_time(block, dtype, kv, G, D):
+    """Rows cut between CTAs, whichever of them finishes last."""
+    g, Hkv, page = gen(G + D), 2, 64
+    lens = [926, 1, 0, 500, 926, 70, 301, 926, 640, 2, 926, 33, 800, 129]
+    n = sum(-(-x // page) for x in lens)
+    k, v = pools(g, n, Hkv, page, D, kv)
+    cache = block.PagedKVCache(k, v, *scales_for(g, kv, Hkv))
+    table, seq = table_for(g, lens, page, n), torch.tensor(lens, dtype=torch.int32, device="cuda")
+    q = rn(g, len(lens), Hkv * G, D, dtype=dtype)
+    first = cache.attend(q, table, seq, return_lse=True)
+    for _ in range(60):
+        again = cache.attend(q, table, seq, return_lse=True)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
 def test_attend_empty_batches(block):
     g = gen(5)
     k, v = pools(g, 4, 2, 16, 64, BF)
